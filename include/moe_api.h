@@ -312,6 +312,109 @@ int moe_bias_update(const int32_t* offsets, int32_t E, float eta, float* corr_bi
 int moe_forward_noalloc(const moe_dims* dims, const moe_weights* w, const uint16_t* x, uint16_t* out,
                         hipStream_t stream);
 
+/* ---- the experts' products on their own, their gradients, 8-bit experts ---- */
+
+/* Sizes of a product over R rows grouped by expert, W[e] an [N, K] weight.
+ * offsets (device [E+1] int32, as moe_permute and moe_workspace_layout.offsets
+ * leave them): the rows of expert e are [offsets[e], offsets[e+1]). Offsets
+ * outside [0, R] or descending are read as their running maximum clamped to
+ * [0, R], so no row outside the tensors is touched; rows before offsets[0] or
+ * from offsets[E] on belong to no expert: they are not read, and the rows of an
+ * output there are left as they were (zero_rest = 0) or set to zero.
+ * Row strides in elements, 0 for dense rows: ldx of x [R, K], ldy of y and dy
+ * [R, N], ldw of a weight's rows and w_stride from one expert's weight to the
+ * next, lddx of dx [R, K].
+ * MOE_ERR_INVALID: R < 0, E, N or K <= 0, a stride below its row's length (w_stride:
+ * below the weight's extent), null or not 16-byte aligned tensors.
+ * MOE_ERR_UNSUPPORTED: N, K or a stride not a multiple of 8 (the kernels move 16
+ * bytes per lane; K a multiple of 16 for the 8-bit product), E > 1024,
+ * R >= 2^31, a row stride >= 2^22, a product of 2^31 tiles or more.
+ * Outputs may not overlap inputs. R = 0 is valid (its row tensors may be null). */
+typedef struct moe_grouped_dims {
+  int64_t R;
+  int32_t E, N, K;
+  int64_t ldx, ldy, ldw, w_stride, lddx;
+  int32_t zero_rest;
+} moe_grouped_dims;
+
+/* Bytes of the workspace (256-byte aligned, device) of the calls below that
+ * take a moe_grouped_dims; 0 for dims they refuse. Nothing in it has to be
+ * zero, and nothing in it is used by a later call: calls that overlap in time
+ * need a workspace each. */
+size_t moe_grouped_workspace_bytes(const moe_grouped_dims* dims);
+
+/* y[r, n] = sum_k x[r, k] W[e(r)][n, k]: x, w, y device bf16, fp32 sums, one
+ * rounding. Asynchronous on `stream`, as every call here. */
+int moe_grouped_matmul(const moe_grouped_dims* dims, const uint16_t* x, const uint16_t* w, const int32_t* offsets,
+                       uint16_t* y, void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* Element types of outputs and gradient tensors. */
+enum moe_dtype { MOE_BF16 = 0, MOE_FP32 = 1 };
+
+/* Gradients of moe_grouped_matmul, dy [R, N] bf16:
+ *   dx[r, k]    = sum_n dy[r, n] W[e(r)][n, k]               bf16 [R, K]
+ *   dw[e][n, k] = sum_{r of e} dy[r, n] x[r, k]              bf16 or fp32, dense [E, N, K]
+ * each with fp32 sums. Either output may be NULL (then it is not computed, and
+ * w, or x, is not read and may be NULL). accumulate != 0: dw is added to what it
+ * holds (in fp32, with one rounding); else experts without rows get zeros. */
+int moe_grouped_matmul_grad(const moe_grouped_dims* dims, const uint16_t* dy, const uint16_t* x, const uint16_t* w,
+                            const int32_t* offsets, uint16_t* dx, void* dw, int32_t dw_dtype, int32_t accumulate,
+                            void* ws, size_t ws_bytes, hipStream_t stream);
+
+/* 8-bit operands: OCP E4M3 codes (one byte each) with one fp32 scale per block,
+ * value = element(code) * scale. The quantisers take the scale 2^e, e the least
+ * integer >= -126 with max|v| <= 448 * 2^e over the block's finite values (-126
+ * for a block of zeros), and round v * 2^-e to the nearest E4M3 value, ties to
+ * even; infinities and NaN become NaN codes.
+ *   rows:   x [R, K] bf16 (row stride ldx, 0 dense), blocks of 128 consecutive
+ *           k: codes [R, K], scales [ceil(K/128), R] (a row of scales per block:
+ *           a product's tile reads those of its rows as one line)
+ *   blocks: w [count, N, K] bf16 dense, blocks of 128 x 128:
+ *           codes [count, N, K], scales [count, ceil(N/128), ceil(K/128)]
+ * MOE_ERR_INVALID: R, count < 0, N, K <= 0, ldx < K, null or not 16-byte aligned
+ * x, w, codes; MOE_ERR_UNSUPPORTED: K or ldx not a multiple of 8, 2^31 blocks or
+ * more, N * K >= 2^31. */
+int moe_quantize_fp8_rows(const uint16_t* x, int64_t R, int32_t K, int64_t ldx, uint8_t* codes, float* scales,
+                          hipStream_t stream);
+int moe_quantize_fp8_blocks(const uint16_t* w, int64_t count, int32_t N, int32_t K, uint8_t* codes, float* scales,
+                            hipStream_t stream);
+
+/* y[r, n] = sum_b xs[b, r] ws8[e][n/128, b] sum_{k in block b} xq[r, k] wq[e][n, k]
+ * with xq, xs as moe_quantize_fp8_rows leaves them and wq [E, N, K] codes,
+ * w_scale [E, ceil(N/128), ceil(K/128)] (any fp32 scales, not only powers of
+ * two). A block's products are summed in fp32, scaled by the product of the two
+ * scales and added in fp32; y bf16, one rounding. Of the dims' strides only ldy is read. */
+int moe_grouped_matmul_fp8(const moe_grouped_dims* dims, const uint8_t* xq, const float* xs, const uint8_t* wq,
+                           const float* w_scale, const int32_t* offsets, uint16_t* y, void* ws, size_t ws_bytes,
+                           hipStream_t stream);
+
+/* ---- the end of a training step: global gradient norm and clipping ---- */
+
+/* One gradient tensor: n elements of dtype (moe_dtype) at `grad` (device,
+ * aligned to its element), contiguous. n = 0 is valid. `out`: where the scaled
+ * gradient goes, of the same type and length; NULL or equal to grad: in place. */
+typedef struct moe_grad_tensor {
+  const void* grad;
+  void* out;
+  int64_t n;
+  int32_t dtype;
+} moe_grad_tensor;
+
+/* norm = sqrt(sum of all tensors' squares), summed in float64 (in an order that
+ * the sizes fix) and rounded once to fp32, on the device.
+ * moe_clip_grad_norm also writes out = grad * (max_norm / norm), one rounding, if
+ * norm > max_norm and norm is finite, and out = grad otherwise. The host array
+ * `tensors` is read during the call only. Nothing waits for the GPU.
+ * MOE_ERR_INVALID: count < 0, null tensors with count > 0, a null, misaligned or
+ * negative-length tensor, an unknown dtype, max_norm negative or NaN, a null
+ * norm, or (clip) outputs that overlap each other or another gradient.
+ * MOE_ERR_UNSUPPORTED: more than 2^40 elements. ws: 256-byte aligned. */
+size_t moe_grad_norm_workspace_bytes(const moe_grad_tensor* tensors, int32_t count);
+int moe_grad_norm(const moe_grad_tensor* tensors, int32_t count, float* norm, void* ws, size_t ws_bytes,
+                  hipStream_t stream);
+int moe_clip_grad_norm(const moe_grad_tensor* tensors, int32_t count, float max_norm, float* norm, void* ws,
+                       size_t ws_bytes, hipStream_t stream);
+
 /* Human-readable text of a status code (static storage). */
 const char* moe_status_string(int status);
 

@@ -25,6 +25,8 @@ __all__ = [
     "MoEError", "MoEDims", "load_library", "library_path", "EXPORTS", "route", "permute", "forward",
     "workspace_bytes", "route_workspace_bytes", "permute_workspace_bytes", "workspace_layout",
     "LatentMoE", "PhaseEvents", "forward_profiled", "PHASES", "forward_noalloc", "NOALLOC_SCRATCH_BYTES",
+    "grouped_matmul", "grouped_matmul_grad", "quantize_fp8_rows", "quantize_fp8_blocks", "grouped_matmul_fp8",
+    "grouped_workspace_bytes", "grad_norm", "clip_grad_norm",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -36,7 +38,9 @@ EXPORTS = (
     "moe_workspace_bytes", "moe_workspace_layout", "moe_forward", "moe_forward_profiled", "moe_status_string",
     "moe_abi_version", "moe_quantize_mxfp8", "moe_forward_mx", "moe_forward_mx_profiled",
     "moe_rmsnorm", "moe_block_workspace_bytes", "moe_block_forward", "moe_bias_update", "moe_quantize_mxfp4",
-    "moe_forward_noalloc",
+    "moe_forward_noalloc", "moe_grouped_workspace_bytes", "moe_grouped_matmul", "moe_grouped_matmul_grad",
+    "moe_quantize_fp8_rows", "moe_quantize_fp8_blocks", "moe_grouped_matmul_fp8", "moe_grad_norm_workspace_bytes",
+    "moe_grad_norm", "moe_clip_grad_norm",
 )
 
 # MOE_NOALLOC_SCRATCH_BYTES of include/moe_api.h
@@ -65,6 +69,17 @@ class _Weights(ctypes.Structure):
 class _ExpertsMx(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("w_up", "w_up_scale", "w_down", "w_down_scale")] + \
         [("format", ctypes.c_int32)]
+
+
+class _GroupedDims(ctypes.Structure):
+    _fields_ = [("R", ctypes.c_int64), ("E", ctypes.c_int32), ("N", ctypes.c_int32), ("K", ctypes.c_int32),
+                ("ldx", ctypes.c_int64), ("ldy", ctypes.c_int64), ("ldw", ctypes.c_int64),
+                ("w_stride", ctypes.c_int64), ("lddx", ctypes.c_int64), ("zero_rest", ctypes.c_int32)]
+
+
+class _GradTensor(ctypes.Structure):
+    _fields_ = [("grad", ctypes.c_void_p), ("out", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("dtype", ctypes.c_int32)]
 
 
 MX_FORMATS = {"mxfp8": 0, "mxfp4": 1}
@@ -136,6 +151,16 @@ def load_library(path: Optional[str] = None):
                                     vp, vp, vp, sz, vp]),
         "moe_bias_update": (i32, [vp, ctypes.c_int32, ctypes.c_float, vp, vp]),
         "moe_forward_noalloc": (i32, [dims_p, ctypes.POINTER(_Weights), vp, vp, vp]),
+        "moe_grouped_workspace_bytes": (sz, [ctypes.POINTER(_GroupedDims)]),
+        "moe_grouped_matmul": (i32, [ctypes.POINTER(_GroupedDims), vp, vp, vp, vp, vp, sz, vp]),
+        "moe_grouped_matmul_grad": (i32, [ctypes.POINTER(_GroupedDims), vp, vp, vp, vp, vp, vp, ctypes.c_int32,
+                                          ctypes.c_int32, vp, sz, vp]),
+        "moe_quantize_fp8_rows": (i32, [vp, ctypes.c_int64, ctypes.c_int32, ctypes.c_int64, vp, vp, vp]),
+        "moe_quantize_fp8_blocks": (i32, [vp, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, vp, vp, vp]),
+        "moe_grouped_matmul_fp8": (i32, [ctypes.POINTER(_GroupedDims), vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "moe_grad_norm_workspace_bytes": (sz, [ctypes.POINTER(_GradTensor), ctypes.c_int32]),
+        "moe_grad_norm": (i32, [ctypes.POINTER(_GradTensor), ctypes.c_int32, vp, vp, sz, vp]),
+        "moe_clip_grad_norm": (i32, [ctypes.POINTER(_GradTensor), ctypes.c_int32, ctypes.c_float, vp, vp, sz, vp]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -513,6 +538,280 @@ def bias_update(offsets, corr_bias, eta: float, *, stream=None):
     _need(offsets, "offsets", torch.int32, (E + 1,), dev)
     _check(load_library().moe_bias_update(_ptr(offsets), E, eta, _ptr(corr_bias), _stream(stream)))
     return corr_bias
+
+
+# ----------------------------------------------------------------------------
+# the experts' products on their own, their gradients, 8-bit experts
+# ----------------------------------------------------------------------------
+
+class _on:
+    """Makes ``device`` current and allocates on ``stream`` (default: the device's current
+    stream), so that scratch freed on return is reused in that stream's order."""
+
+    def __init__(self, device, stream):
+        torch = _torch()
+        if device.type != "cuda":
+            raise ValueError(f"tensors must be on the GPU, got {device}")
+        if stream is not None and stream.device != device:
+            raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
+        self._ctx = torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
+        self._device = device
+        self._given = stream
+
+    def __enter__(self):
+        self._ctx.__enter__()
+        s = self._given if self._given is not None else _torch().cuda.current_stream(self._device)
+        return s.cuda_stream
+
+    def __exit__(self, *exc):
+        return self._ctx.__exit__(*exc)
+
+
+def _need_rows(t, name, dtype, shape, device):
+    """A matrix [rows, cols] whose columns are contiguous; returns its row stride."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on the GPU device {device}")
+    if shape[0] <= 1:
+        if shape[1] > 1 and t.stride(1) != 1 and t.numel():
+            raise ValueError(f"{name}'s columns must be contiguous")
+        return shape[1]
+    if (shape[1] > 1 and t.stride(1) != 1) or t.stride(0) < shape[1]:
+        raise ValueError(f"{name} must have contiguous columns and a row stride of at least {shape[1]}, "
+                         f"got strides {tuple(t.stride())}")
+    return t.stride(0)
+
+
+def _grouped_shapes(x, w, offsets):
+    torch = _torch()
+    for t, name, nd in ((x, "x", 2), (w, "w", 3), (offsets, "offsets", 1)):
+        if not isinstance(t, torch.Tensor):
+            raise TypeError(f"{name} must be a torch tensor")
+        if t.dim() != nd:
+            raise ValueError(f"{name} must have {nd} dimensions, got shape {tuple(t.shape)}")
+    E, N, K = w.shape
+    _need(offsets, "offsets", torch.int32, (E + 1,), w.device)
+    return E, N, K
+
+
+def _weight_strides(w, dtype, device):
+    """Row and expert strides of w [E, N, K]."""
+    E, N, K = w.shape
+    if w.dtype != dtype:
+        raise TypeError(f"w must be {dtype}, got {w.dtype}")
+    if w.device != device:
+        raise ValueError(f"w must be on the GPU device {device}")
+    ldw = w.stride(1) if N > 1 else K
+    es = w.stride(0) if E > 1 else N * ldw
+    if (K > 1 and w.stride(2) != 1) or ldw < K or es < (N - 1) * ldw + K:
+        raise ValueError(f"w must hold separate [N, K] matrices with contiguous rows, got strides {tuple(w.stride())}")
+    return ldw, es
+
+
+def _grouped_ws(d: _GroupedDims, device, ws):
+    nbytes = load_library().moe_grouped_workspace_bytes(ctypes.byref(d))
+    return _workspace(nbytes, device, ws)
+
+
+def grouped_workspace_bytes(R: int, E: int, N: int, K: int) -> int:
+    """Workspace of the grouped calls on R rows and E weights [N, K]."""
+    return int(load_library().moe_grouped_workspace_bytes(ctypes.byref(_GroupedDims(R, E, N, K))))
+
+
+def grouped_matmul(x, w, offsets, *, out=None, ws=None, stream=None):
+    """moe_grouped_matmul: y[r] = x[r] . w[e]^T for the rows offsets[e] <= r < offsets[e+1].
+
+    x [R, K] and w [E, N, K] bf16 (rows contiguous, strides multiples of 8), offsets [E+1]
+    int32 on the device (``permute``, or the forward's). Returns y [R, N] bf16; rows that
+    belong to no expert are left as they are in ``out`` (zero when it is not given)."""
+    torch = _torch()
+    E, N, K = _grouped_shapes(x, w, offsets)
+    R, dev = x.shape[0], x.device
+    ldx = _need_rows(x, "x", torch.bfloat16, (R, K), dev)
+    ldw, es = _weight_strides(w, torch.bfloat16, dev)
+    with _on(dev, stream) as st:
+        fresh = out is None
+        if fresh:
+            out = torch.empty(R, N, dtype=torch.bfloat16, device=dev)
+        ldy = _need_rows(out, "out", torch.bfloat16, (R, N), dev)
+        d = _GroupedDims(R, E, N, K, ldx, ldy, ldw, es, 0, int(fresh))
+        wsp = _grouped_ws(d, dev, ws)
+        _check(load_library().moe_grouped_matmul(ctypes.byref(d), _ptr(x), _ptr(w), _ptr(offsets), _ptr(out),
+                                                 _ptr(wsp), wsp.numel() * wsp.element_size(), st))
+    return out
+
+
+def grouped_matmul_grad(dy, x, w, offsets, *, need_dx: bool = True, need_dw: bool = True, dx=None, dw=None,
+                        dw_dtype=None, accumulate: bool = False, ws=None, stream=None):
+    """moe_grouped_matmul_grad: the gradients (dx, dw) of ``grouped_matmul`` given dy [R, N] bf16.
+
+    dx [R, K] bf16 (rows without an expert as in ``grouped_matmul``); dw [E, N, K] in
+    ``dw_dtype`` (bf16 by default, or fp32), zero for experts without rows. ``accumulate``
+    adds to the ``dw`` given. need_dx / need_dw False: that gradient is not computed (None)."""
+    torch = _torch()
+    E, N, K = _grouped_shapes(x, w, offsets)
+    R, dev = x.shape[0], x.device
+    ldx = _need_rows(x, "x", torch.bfloat16, (R, K), dev)
+    if not isinstance(dy, torch.Tensor) or dy.dim() != 2:
+        raise TypeError("dy must be a [R, N] torch tensor")
+    ldy = _need_rows(dy, "dy", torch.bfloat16, (R, N), dev)
+    ldw, es = _weight_strides(w, torch.bfloat16, dev)
+    if not (need_dx or need_dw):
+        raise ValueError("one of need_dx and need_dw must be set")
+    if accumulate and (dw is None or not need_dw):
+        raise ValueError("accumulate needs the dw to add to")
+    if dw_dtype is None:
+        dw_dtype = dw.dtype if dw is not None else torch.bfloat16
+    if dw_dtype not in (torch.bfloat16, torch.float32):
+        raise TypeError(f"dw_dtype must be bfloat16 or float32, got {dw_dtype}")
+    with _on(dev, stream) as st:
+        lddx, fresh = 0, dx is None
+        if need_dx:
+            if fresh:
+                dx = torch.empty(R, K, dtype=torch.bfloat16, device=dev)
+            lddx = _need_rows(dx, "dx", torch.bfloat16, (R, K), dev)
+        if need_dw:
+            if dw is None:
+                dw = torch.empty(E, N, K, dtype=dw_dtype, device=dev)
+            _need(dw, "dw", dw_dtype, (E, N, K), dev)
+        d = _GroupedDims(R, E, N, K, ldx, ldy, ldw, es, lddx, int(fresh))
+        wsp = _grouped_ws(d, dev, ws)
+        _check(load_library().moe_grouped_matmul_grad(
+            ctypes.byref(d), _ptr(dy), _ptr(x), _ptr(w), _ptr(offsets), _ptr(dx) if need_dx else None,
+            _ptr(dw) if need_dw else None, 1 if dw_dtype == torch.float32 else 0, int(accumulate), _ptr(wsp),
+            wsp.numel() * wsp.element_size(), st))
+    return (dx if need_dx else None), (dw if need_dw else None)
+
+
+def quantize_fp8_rows(x, *, stream=None):
+    """moe_quantize_fp8_rows: x [R, K] bf16 -> (codes uint8 [R, K], scales fp32 [ceil(K/128), R])."""
+    torch = _torch()
+    if not isinstance(x, torch.Tensor) or x.dim() != 2:
+        raise TypeError("x must be a [R, K] torch tensor")
+    R, K = x.shape
+    ldx = _need_rows(x, "x", torch.bfloat16, (R, K), x.device)
+    with _on(x.device, stream) as st:
+        codes = torch.empty(R, K, dtype=torch.uint8, device=x.device)
+        scales = torch.empty((K + 127) // 128, R, dtype=torch.float32, device=x.device)
+        _check(load_library().moe_quantize_fp8_rows(_ptr(x), R, K, ldx, _ptr(codes), _ptr(scales), st))
+    return codes, scales
+
+
+def quantize_fp8_blocks(w, *, stream=None):
+    """moe_quantize_fp8_blocks: w [..., N, K] bf16 contiguous -> (codes uint8 [..., N, K],
+    scales fp32 [..., ceil(N/128), ceil(K/128)])."""
+    torch = _torch()
+    if not isinstance(w, torch.Tensor) or w.dim() < 2 or w.dtype != torch.bfloat16:
+        raise TypeError("w must be a [..., N, K] bf16 torch tensor")
+    _need(w, "w", torch.bfloat16, w.shape, w.device)
+    N, K = w.shape[-2:]
+    count = w.numel() // (N * K) if N * K else 0
+    with _on(w.device, stream) as st:
+        codes = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
+        scales = torch.empty(w.shape[:-2] + ((N + 127) // 128, (K + 127) // 128), dtype=torch.float32,
+                             device=w.device)
+        _check(load_library().moe_quantize_fp8_blocks(_ptr(w), count, N, K, _ptr(codes), _ptr(scales), st))
+    return codes, scales
+
+
+def grouped_matmul_fp8(x, w_codes, w_scale, offsets, *, x_scale=None, out=None, ws=None, stream=None):
+    """moe_grouped_matmul_fp8: the grouped product on E4M3 weights (``quantize_fp8_blocks``, or
+    codes [E, N, K] with any fp32 scales [E, ceil(N/128), ceil(K/128)]).
+
+    x: [R, K] bf16, quantised here (``quantize_fp8_rows``), or its codes with ``x_scale``
+    given. K a multiple of 16. Returns y [R, N] bf16."""
+    torch = _torch()
+    E, N, K = _grouped_shapes(x, w_codes, offsets)
+    R, dev = x.shape[0], x.device
+    kb, nb = (K + 127) // 128, (N + 127) // 128
+    _need(w_codes, "w_codes", torch.uint8, (E, N, K), dev)
+    _need(w_scale, "w_scale", torch.float32, (E, nb, kb), dev)
+    if x_scale is None:
+        _need_rows(x, "x", torch.bfloat16, (R, K), dev)
+    else:
+        _need(x, "x", torch.uint8, (R, K), dev)
+        _need(x_scale, "x_scale", torch.float32, (kb, R), dev)
+    with _on(dev, stream) as st:
+        fresh = out is None
+        if fresh:
+            out = torch.empty(R, N, dtype=torch.bfloat16, device=dev)
+        ldy = _need_rows(out, "out", torch.bfloat16, (R, N), dev)
+        if x_scale is None:
+            x, x_scale = quantize_fp8_rows(x, stream=stream)
+        d = _GroupedDims(R, E, N, K, 0, ldy, 0, 0, 0, int(fresh))
+        wsp = _grouped_ws(d, dev, ws)
+        _check(load_library().moe_grouped_matmul_fp8(ctypes.byref(d), _ptr(x), _ptr(x_scale), _ptr(w_codes),
+                                                     _ptr(w_scale), _ptr(offsets), _ptr(out), _ptr(wsp),
+                                                     wsp.numel() * wsp.element_size(), st))
+    return out
+
+
+# ----------------------------------------------------------------------------
+# the end of a training step: global gradient norm and clipping
+# ----------------------------------------------------------------------------
+
+def _grad_table(grads, out):
+    torch = _torch()
+    grads = list(grads)
+    out = None if out is None else list(out)
+    if out is not None and len(out) != len(grads):
+        raise ValueError(f"out must hold one tensor for each of the {len(grads)} gradients, got {len(out)}")
+    if not grads:
+        raise ValueError("grads must hold at least one tensor")
+    dev = grads[0].device if isinstance(grads[0], torch.Tensor) else None
+    kinds = {torch.bfloat16: 0, torch.float32: 1}
+    tab = (_GradTensor * len(grads))()
+    for i, g in enumerate(grads):
+        if not isinstance(g, torch.Tensor) or g.dtype not in kinds:
+            raise TypeError(f"gradient {i} must be a bf16 or fp32 torch tensor")
+        if g.device != dev or not g.is_cuda:
+            raise ValueError(f"gradient {i} must be on the GPU device {dev}")
+        if not g.is_contiguous():
+            raise ValueError(f"gradient {i} must be contiguous")
+        o = None
+        if out is not None:
+            o = out[i]
+            if not isinstance(o, torch.Tensor) or o.dtype != g.dtype or o.shape != g.shape or o.device != dev \
+                    or not o.is_contiguous():
+                raise ValueError(f"out {i} must be a contiguous {g.dtype} tensor of shape {tuple(g.shape)} on {dev}")
+        e = tab[i]
+        e.grad, e.out, e.n, e.dtype = g.data_ptr(), None if o is None else o.data_ptr(), g.numel(), kinds[g.dtype]
+    return tab, len(grads), dev
+
+
+def grad_norm(grads, *, ws=None, stream=None):
+    """moe_grad_norm: sqrt of the sum of squares over all ``grads`` (bf16 and fp32 tensors on one
+    GPU, contiguous) as a 0-dimensional fp32 tensor on that GPU."""
+    torch = _torch()
+    tab, n, dev = _grad_table(grads, None)
+    lib = load_library()
+    with _on(dev, stream) as st:
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+        nbytes = lib.moe_grad_norm_workspace_bytes(tab, n)
+        w = _workspace(nbytes, dev, ws)
+        _check(lib.moe_grad_norm(tab, n, _ptr(norm), _ptr(w), w.numel() * w.element_size(), st))
+    return norm
+
+
+def clip_grad_norm(grads, max_norm: float, *, out=None, ws=None, stream=None):
+    """moe_clip_grad_norm: scales ``grads`` by max_norm / norm where their global norm is finite and
+    above max_norm, in place or into ``out`` (one tensor for each). Returns the norm before the
+    clip as a 0-dimensional fp32 tensor on the GPU; nothing waits for it."""
+    torch = _torch()
+    tab, n, dev = _grad_table(grads, out)
+    lib = load_library()
+    with _on(dev, stream) as st:
+        norm = torch.empty((), dtype=torch.float32, device=dev)
+        nbytes = lib.moe_grad_norm_workspace_bytes(tab, n)
+        w = _workspace(nbytes, dev, ws)
+        _check(lib.moe_clip_grad_norm(tab, n, max_norm, _ptr(norm), _ptr(w), w.numel() * w.element_size(), st))
+    return norm
 
 
 class PhaseEvents:

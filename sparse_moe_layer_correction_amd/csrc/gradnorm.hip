@@ -1,0 +1,156 @@
+// The global norm of many gradient tensors, and their clipping.
+//
+//   norm = sqrt(sum over all tensors of g^2);  out = g * (max_norm / norm) where norm > max_norm
+//
+// Bound by HBM: the gradients are read once for the norm and, where it passes
+// the bound, once more to be scaled (the norm is needed before the first of
+// them can be). Squares are summed in float64: no finite gradient overflows,
+// and the sum of 10^10 terms keeps every bit of the fp32 result. The order of
+// the sums is fixed by the sizes alone (a thread's own elements, the wave, the
+// workgroup, then the workgroups' partials in order), so a call repeats bit
+// for bit.
+//
+// The tensors' addresses travel in the kernel arguments (kGradTableSize a
+// launch): nothing is copied to the device, and nothing of them is kept.
+#include "grouped_ops.h"
+
+namespace moe {
+
+constexpr int kGradThreads = 256;
+
+__device__ __forceinline__ double block_sum_f64(double v, double* part) {
+#pragma unroll
+  for (int m = 32; m >= 1; m >>= 1) v += __shfl_xor(v, m, kWave);
+  const int wave = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 0) part[wave] = v;
+  __syncthreads();
+  double s = part[0];
+  for (int w = 1; w < (int)blockDim.x / kWave; ++w) s += part[w];
+  __syncthreads();
+  return s;
+}
+
+__device__ __forceinline__ double sq2(uint32_t w) {
+  const double a = (double)bf16_bits_to_f32(w & 0xFFFFu), b = (double)bf16_bits_to_f32(w >> 16);
+  return a * a + b * b;
+}
+
+// the table entry that holds chunk c: the last one that starts at or before it
+__device__ __forceinline__ int grad_entry(const GradTable& t, int c) {
+  int lo = 0, hi = t.count - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (t.first[mid] <= c) lo = mid;
+    else hi = mid - 1;
+  }
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+
+// elements of a chunk that come before its first 16-byte boundary
+template <typename T>
+__device__ __forceinline__ int head_of(const T* p, int n) {
+  const int mis = (int)(((16 - (reinterpret_cast<uintptr_t>(p) & 15)) & 15) / sizeof(T));
+  return min(mis, n);
+}
+
+__global__ void __launch_bounds__(kGradThreads) grad_sumsq_kernel(const GradTable t, double* __restrict__ partial) {
+  __shared__ double part[kGradThreads / kWave];
+  double s = 0.0;
+  for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+    const int i = grad_entry(t, c);
+    const int64_t at = (int64_t)(c - t.first[i]) * kGradChunk;
+    const int n = (int)min((int64_t)kGradChunk, t.n[i] - at);
+    if ((t.f32[i >> 5] >> (i & 31)) & 1) {
+      const float* p = static_cast<const float*>(t.src[i]) + at;
+      const int h = head_of(p, n), nv = (n - h) / 4, tail = h + nv * 4;
+      const f32x4* v = reinterpret_cast<const f32x4*>(p + h);
+      for (int j = threadIdx.x; j < nv; j += kGradThreads) {
+        const f32x4 q = v[j];
+        s += (double)q[0] * q[0] + (double)q[1] * q[1] + (double)q[2] * q[2] + (double)q[3] * q[3];
+      }
+      if ((int)threadIdx.x < h) s += (double)p[threadIdx.x] * p[threadIdx.x];
+      if (tail + (int)threadIdx.x < n) s += (double)p[tail + threadIdx.x] * p[tail + threadIdx.x];
+    } else {
+      const uint16_t* p = static_cast<const uint16_t*>(t.src[i]) + at;
+      const int h = head_of(p, n), nv = (n - h) / 8, tail = h + nv * 8;
+      const u32x4* v = reinterpret_cast<const u32x4*>(p + h);
+      for (int j = threadIdx.x; j < nv; j += kGradThreads) {
+        const u32x4 q = v[j];
+        s += sq2(q[0]) + sq2(q[1]) + sq2(q[2]) + sq2(q[3]);
+      }
+      if ((int)threadIdx.x < h) s += sq2(p[threadIdx.x]);
+      if (tail + (int)threadIdx.x < n) s += sq2(p[tail + threadIdx.x]);
+    }
+  }
+  s = block_sum_f64(s, part);
+  if (threadIdx.x == 0) partial[blockIdx.x] = s;
+}
+
+// partials -> norm and the factor the gradients take
+__global__ void __launch_bounds__(1024) grad_norm_kernel(const double* __restrict__ partial, int n, double max_norm,
+                                                         float* __restrict__ norm, double* __restrict__ factor) {
+  __shared__ double part[16];
+  double s = 0.0;
+  for (int i = threadIdx.x; i < n; i += 1024) s += partial[i];
+  s = block_sum_f64(s, part);
+  if (threadIdx.x == 0) {
+    const double v = __builtin_sqrt(s);
+    *norm = (float)v;
+    // a norm that is not finite leaves the gradients as they are
+    if (factor != nullptr) *factor = v > max_norm && v < __builtin_inf() ? max_norm / v : 1.0;
+  }
+}
+
+__global__ void __launch_bounds__(kGradThreads) grad_scale_kernel(const GradTable t, const double* __restrict__ factor) {
+  const double f = *factor;
+  for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+    const int i = grad_entry(t, c);
+    if (f == 1.0 && t.src[i] == t.dst[i]) continue;      // in place and nothing to scale
+    const int64_t at = (int64_t)(c - t.first[i]) * kGradChunk;
+    const int n = (int)min((int64_t)kGradChunk, t.n[i] - at);
+    if ((t.f32[i >> 5] >> (i & 31)) & 1) {
+      const float* p = static_cast<const float*>(t.src[i]) + at;
+      float* o = static_cast<float*>(t.dst[i]) + at;
+      const bool same = ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(o)) & 15) == 0;
+      const int h = same ? head_of(p, n) : n, nv = (n - h) / 4, tail = h + nv * 4;
+      for (int j = threadIdx.x; j < nv; j += kGradThreads) {
+        f32x4 q = reinterpret_cast<const f32x4*>(p + h)[j];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) q[k] = (float)((double)q[k] * f);
+        reinterpret_cast<f32x4*>(o + h)[j] = q;
+      }
+      for (int j = threadIdx.x; j < h; j += kGradThreads) o[j] = (float)((double)p[j] * f);
+      for (int j = tail + threadIdx.x; j < n; j += kGradThreads) o[j] = (float)((double)p[j] * f);
+    } else {
+      const uint16_t* p = static_cast<const uint16_t*>(t.src[i]) + at;
+      uint16_t* o = static_cast<uint16_t*>(t.dst[i]) + at;
+      const bool same = ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(o)) & 15) == 0;
+      const int h = same ? head_of(p, n) : n, nv = (n - h) / 8, tail = h + nv * 8;
+      auto one = [&](uint32_t b) { return (float)((double)bf16_bits_to_f32(b) * f); };
+      for (int j = threadIdx.x; j < nv; j += kGradThreads) {
+        u32x4 q = reinterpret_cast<const u32x4*>(p + h)[j];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) q[k] = cvt_pk_bf16(one(q[k] & 0xFFFFu), one(q[k] >> 16));
+        reinterpret_cast<u32x4*>(o + h)[j] = q;
+      }
+      for (int j = threadIdx.x; j < h; j += kGradThreads) o[j] = (uint16_t)cvt_pk_bf16(one(p[j]), 0.f);
+      for (int j = tail + threadIdx.x; j < n; j += kGradThreads) o[j] = (uint16_t)cvt_pk_bf16(one(p[j]), 0.f);
+    }
+  }
+}
+
+hipError_t launch_grad_sumsq(const GradTable& t, int blocks, double* partial, hipStream_t st) {
+  hipLaunchKernelGGL(grad_sumsq_kernel, dim3(blocks), dim3(kGradThreads), 0, st, t, partial);
+  return hipGetLastError();
+}
+hipError_t launch_grad_norm(const double* partial, int n, double max_norm, float* norm, double* factor,
+                            hipStream_t st) {
+  hipLaunchKernelGGL(grad_norm_kernel, dim3(1), dim3(1024), 0, st, partial, n, max_norm, norm, factor);
+  return hipGetLastError();
+}
+hipError_t launch_grad_scale(const GradTable& t, int blocks, const double* factor, hipStream_t st) {
+  hipLaunchKernelGGL(grad_scale_kernel, dim3(blocks), dim3(kGradThreads), 0, st, t, factor);
+  return hipGetLastError();
+}
+
+}  // namespace moe

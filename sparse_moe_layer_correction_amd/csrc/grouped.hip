@@ -1,0 +1,120 @@
+// Tile table and launchers of the grouped products (grouped.h).
+#include "grouped.h"
+#include "grouped_ops.h"
+
+namespace moe {
+
+// Rows of each expert from its offsets, and the M tile table of a product with
+// BM-row tiles. offsets that fall, or lie outside [0, R], are read as their
+// running maximum clamped to [0, R]: ranges then never overlap, their tiles
+// never pass R / BM + E, and no kernel touches a row outside [0, R). One
+// workgroup, thread e for expert e (E <= 1024): two scans over the waves. The
+// workgroups after it (kRestBlocks, launched where rest is asked for) zero the
+// output's rows before the first expert's and after the last one's.
+constexpr int kRestBlocks = 64;
+__global__ void __launch_bounds__(1024) grouped_tiles_kernel(const int32_t* __restrict__ offsets, int E, int R, int BM,
+                                                             int2* __restrict__ ranges, TileRec* __restrict__ tiles,
+                                                             int32_t* __restrict__ n_mtiles,
+                                                             int32_t* __restrict__ counters, const RestRows rest) {
+  __shared__ int wmax[16], wsum[16];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  auto clamped = [&](int i) { return min(max(offsets[min(i, E)], 0), R); };
+  int v = clamped(tid);
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    const int o = __shfl_up(v, d, kWave);
+    if (lane >= d) v = max(v, o);
+  }
+  if (lane == 63) wmax[wave] = v;
+  if (blockIdx.x == 0 && tid < kGemmCounters) counters[tid] = 0;
+  __syncthreads();
+  for (int w = 0; w < wave; ++w) v = max(v, wmax[w]);
+  if (blockIdx.x > 0) {
+    int end = 0;                                             // the highest offset
+    __shared__ int top;
+    if (tid == E - 1) top = max(v, clamped(E));
+    __syncthreads();
+    end = top;
+    const int cpr = rest.N / 8, begin = clamped(0);
+    const int64_t n = (int64_t)(begin + R - end) * cpr;
+    for (int64_t i = (int64_t)(blockIdx.x - 1) * 1024 + tid; i < n; i += (int64_t)kRestBlocks * 1024) {
+      const int64_t q = i / cpr, r = q < begin ? q : end + (q - begin);
+      *reinterpret_cast<u32x4*>(rest.C + r * rest.ldc + (i - q * cpr) * 8) = u32x4{0u, 0u, 0u, 0u};
+    }
+    return;
+  }
+  const int lo = v;
+  const int hi = tid < E ? max(lo, clamped(tid + 1)) : lo;   // the next expert's start: max with all before it
+  const int nt = (hi - lo + BM - 1) / BM;
+  const int it = wave_inclusive_scan_i32(nt);
+  if (lane == 63) wsum[wave] = it;
+  __syncthreads();
+  int first = it - nt;
+  for (int w = 0; w < wave; ++w) first += wsum[w];
+  if (tid < E) {
+    ranges[tid] = make_int2(lo, hi);
+    if (tiles != nullptr)
+      for (int i = 0; i < nt; ++i) tiles[first + i] = make_int4(tid, first, lo, hi);
+  }
+  if (tid == E - 1) *n_mtiles = first + nt;
+}
+
+hipError_t launch_grouped_tiles(const int32_t* offsets, int E, int R, int BM, const GroupedScratch& s,
+                                const RestRows& rest, hipStream_t st) {
+  hipLaunchKernelGGL(grouped_tiles_kernel, dim3(rest.C && R > 0 ? 1 + kRestBlocks : 1), dim3(1024), 0, st, offsets, E, R,
+                     BM, s.ranges, s.tiles, s.n_mtiles, s.counters, rest);
+  return hipGetLastError();
+}
+
+template <int FORM, int OUT>
+static void launch_form(const GroupedArgs& a, int64_t grid, hipStream_t st) {
+  hipLaunchKernelGGL((grouped_kernel<FORM, 128, 128, 2, 2, 2, OUT>), dim3((unsigned)grid), dim3(256), 0, st, a);
+}
+
+int grouped_bm(int64_t R, int E) { (void)R; (void)E; return 128; }
+
+hipError_t launch_grouped_rows(const GroupedProduct& p, const GroupedScratch& s, int BM, hipStream_t st) {
+  GroupedArgs a{};
+  a.A = p.A;
+  a.B = p.B;
+  a.C = p.C;
+  a.lda = p.lda;
+  a.ldb = p.ldb;
+  a.ldc = p.ldc;
+  a.b_estride = p.estride;
+  a.N = p.N;
+  a.Kd = p.Kd;
+  a.tiles = s.tiles;
+  a.n_mtiles = s.n_mtiles;
+  a.ntiles = (p.N + 127) / 128;
+  const int64_t grid = grouped_max_tiles(p.R, p.E, BM) * a.ntiles;
+  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (p.transposed_b) launch_form<FORM_NN, EPI_BF16>(a, grid, st);
+  else launch_form<FORM_NT, EPI_BF16>(a, grid, st);
+  return hipGetLastError();
+}
+
+hipError_t launch_grouped_wgrad(const GroupedProduct& p, int M, bool f32, bool accumulate, const GroupedScratch& s,
+                                hipStream_t st) {
+  GroupedArgs a{};
+  a.A = p.A;
+  a.B = p.B;
+  a.C = p.C;
+  a.lda = p.lda;
+  a.ldb = p.ldb;
+  a.ldc = p.ldc;
+  a.c_estride = p.estride;
+  a.M = M;
+  a.N = p.N;
+  a.ranges = s.ranges;
+  a.mtiles = (M + 127) / 128;
+  a.ntiles = (p.N + 127) / 128;
+  a.accumulate = accumulate;
+  const int64_t grid = (int64_t)p.E * a.mtiles * a.ntiles;
+  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (f32) launch_form<FORM_TN, EPI_F32>(a, grid, st);
+  else launch_form<FORM_TN, EPI_BF16>(a, grid, st);
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -1,0 +1,80 @@
+// Private declarations shared by the expert operators' kernels and their C ABI layer.
+#pragma once
+
+#include "kernels.h"
+
+namespace moe {
+
+// Device scratch of one grouped call.
+struct GroupedScratch {
+  int2* ranges;        // [E] rows of each expert
+  int4* tiles;         // [grouped_max_tiles] M tile table
+  int32_t* n_mtiles;   // [1]
+  int32_t* counters;   // [kGemmCounters] zeroed by launch_grouped_tiles
+};
+
+// M tiles that R rows in E experts can need
+inline int64_t grouped_max_tiles(int64_t R, int E, int BM) { return R / BM + (R < E ? R : E); }
+
+struct GroupedProduct {
+  const uint16_t *A, *B;
+  void* C;
+  int64_t lda, ldb, ldc;
+  int64_t estride;     // experts' B (rows products), experts' C (wgrad)
+  int64_t R;
+  int E, N, Kd;
+  bool transposed_b;   // B stored [Kd, N]
+};
+
+// Output whose rows of no expert are to be zeroed (C null: none).
+struct RestRows {
+  uint16_t* C;
+  int64_t ldc;
+  int N;               // multiple of 8
+};
+
+int grouped_bm(int64_t R, int E);
+hipError_t launch_grouped_tiles(const int32_t* offsets, int E, int R, int BM, const GroupedScratch& s,
+                                const RestRows& rest, hipStream_t st);
+hipError_t launch_grouped_rows(const GroupedProduct& p, const GroupedScratch& s, int BM, hipStream_t st);
+hipError_t launch_grouped_wgrad(const GroupedProduct& p, int M, bool f32, bool accumulate, const GroupedScratch& s,
+                                hipStream_t st);
+
+// E4M3 codes, one scale per 128 (fp8.h)
+struct Fp8Args {
+  const uint8_t* A;            // [R, K] codes of the rows
+  const float* sx;             // [kb, R]
+  const uint8_t* B;            // [E, N, K] codes of the weights
+  const float* sw;             // [E, nb, kb]
+  uint16_t* C;
+  int64_t ldc, R;
+  int N, K, nb, kb;
+  const int4* tiles;
+  const int32_t* n_mtiles;
+  int ntiles;
+};
+hipError_t launch_fp8_rows(const uint16_t* x, int64_t R, int K, int64_t ldx, uint8_t* codes, float* scales,
+                           hipStream_t st);
+hipError_t launch_fp8_blocks(const uint16_t* w, int64_t count, int N, int K, uint8_t* codes, float* scales,
+                             hipStream_t st);
+hipError_t launch_grouped_fp8(const Fp8Args& a, int64_t R, int E, int BM, hipStream_t st);
+
+// Gradient tensors of one launch; entry i's chunks of kGradChunk elements are
+// first[i] .. first[i + 1] of the launch's (the last entry's end at chunks).
+constexpr int kGradTableSize = 120;
+constexpr int kGradChunk = 1 << 15;
+struct GradTable {
+  const void* src[kGradTableSize];
+  void* dst[kGradTableSize];
+  int64_t n[kGradTableSize];
+  int first[kGradTableSize];
+  uint32_t f32[(kGradTableSize + 31) / 32];   // bit i: entry i is fp32, else bf16
+  int count, chunks;
+};
+static_assert(sizeof(GradTable) <= 4000, "kernel arguments");
+hipError_t launch_grad_sumsq(const GradTable& t, int blocks, double* partial, hipStream_t st);
+hipError_t launch_grad_norm(const double* partial, int n, double max_norm, float* norm, double* factor,
+                            hipStream_t st);
+hipError_t launch_grad_scale(const GradTable& t, int blocks, const double* factor, hipStream_t st);
+
+}  // namespace moe

@@ -1,0 +1,324 @@
+// C ABI of the operators around the layer: the grouped products and their
+// gradients, the 8-bit products and quantisers, gradient norm and clipping.
+// Argument checks, workspace carving and launch sequences; host code only.
+#include "../../include/moe_api.h"
+
+#include <algorithm>
+#include <new>
+#include <utility>
+#include <vector>
+
+#include "grouped_ops.h"
+
+namespace {
+
+using namespace moe;
+
+constexpr size_t kAlign = 256;
+size_t align_up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
+int hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
+bool ws_ok(const void* ws, size_t have, size_t need) {
+  return ws != nullptr && have >= need && (reinterpret_cast<uintptr_t>(ws) % kAlign) == 0;
+}
+bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+// the smallest M tile, which needs the longest table
+constexpr int kMinBM = 64;
+constexpr int64_t kMaxStride = (int64_t)1 << 22;   // 256 rows of 2 bytes stay below 2 GiB
+
+// dims with the dense strides filled in
+int grouped_dims(const moe_grouped_dims* in, moe_grouped_dims* d) {
+  if (in == nullptr) return MOE_ERR_INVALID;
+  *d = *in;
+  if (d->R < 0 || d->E <= 0 || d->N <= 0 || d->K <= 0) return MOE_ERR_INVALID;
+  if (d->ldx < 0 || d->ldy < 0 || d->ldw < 0 || d->w_stride < 0 || d->lddx < 0) return MOE_ERR_INVALID;
+  if (d->ldx == 0) d->ldx = d->K;
+  if (d->ldy == 0) d->ldy = d->N;
+  if (d->ldw == 0) d->ldw = d->K;
+  if (d->lddx == 0) d->lddx = d->K;
+  const int64_t extent = (int64_t)(d->N - 1) * d->ldw + d->K;
+  if (d->w_stride == 0) d->w_stride = (int64_t)d->N * d->ldw;
+  if (d->ldx < d->K || d->ldy < d->N || d->ldw < d->K || d->lddx < d->K || d->w_stride < extent)
+    return MOE_ERR_INVALID;
+  if (d->E > kMaxExperts || d->R > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
+  if ((d->N | d->K) % 8 || (d->ldx | d->ldy | d->ldw | d->w_stride | d->lddx) % 8) return MOE_ERR_UNSUPPORTED;
+  if (std::max(std::max(d->ldx, d->ldy), std::max(d->ldw, d->lddx)) >= kMaxStride) return MOE_ERR_UNSUPPORTED;
+  // tiles of the three products, counted with the smallest tile
+  const int64_t nt = (d->N + kMinBM - 1) / kMinBM, kt = (d->K + kMinBM - 1) / kMinBM;
+  if (grouped_max_tiles(d->R, d->E, kMinBM) * std::max(nt, kt) > 0x7FFFFFFF || (int64_t)d->E * nt * kt > 0x7FFFFFFF)
+    return MOE_ERR_UNSUPPORTED;
+  return MOE_OK;
+}
+
+struct GroupedLayout {
+  size_t counters, n_mtiles, ranges, tiles, total;
+};
+
+GroupedLayout grouped_layout(const moe_grouped_dims& d) {
+  GroupedLayout l{};
+  size_t o = 0;
+  auto take = [&](size_t bytes) { const size_t at = o; o = align_up(o + bytes); return at; };
+  l.counters = take(kGemmCounters * 4);
+  l.n_mtiles = take(4);
+  l.ranges = take((size_t)d.E * 8);
+  l.tiles = take((size_t)grouped_max_tiles(d.R, d.E, kMinBM) * 16);
+  l.total = o;
+  return l;
+}
+
+GroupedScratch grouped_scratch(const GroupedLayout& l, void* ws) {
+  char* p = static_cast<char*>(ws);
+  return GroupedScratch{reinterpret_cast<int2*>(p + l.ranges), reinterpret_cast<int4*>(p + l.tiles),
+                        reinterpret_cast<int32_t*>(p + l.n_mtiles), reinterpret_cast<int32_t*>(p + l.counters)};
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_grouped_workspace_bytes(const moe_grouped_dims* dims) {
+  moe_grouped_dims d;
+  if (grouped_dims(dims, &d) != MOE_OK) return 0;
+  return grouped_layout(d).total;
+}
+
+int moe_grouped_matmul(const moe_grouped_dims* dims, const uint16_t* x, const uint16_t* w, const int32_t* offsets,
+                       uint16_t* y, void* ws, size_t ws_bytes, hipStream_t stream) {
+  moe_grouped_dims d;
+  const int st = grouped_dims(dims, &d);
+  if (st != MOE_OK) return st;
+  if (!w || !offsets || (d.R > 0 && (!x || !y))) return MOE_ERR_INVALID;
+  if (!aligned16(x) || !aligned16(w) || !aligned16(y)) return MOE_ERR_INVALID;
+  const GroupedLayout l = grouped_layout(d);
+  if (!ws_ok(ws, ws_bytes, l.total)) return MOE_ERR_WORKSPACE;
+  if (d.R == 0) return MOE_OK;
+  const GroupedScratch s = grouped_scratch(l, ws);
+  const int BM = grouped_bm(d.R, d.E);
+  const RestRows rest{d.zero_rest ? y : nullptr, d.ldy, d.N};
+  if (launch_grouped_tiles(offsets, d.E, (int)d.R, BM, s, rest, stream) != hipSuccess) return MOE_ERR_HIP;
+  const GroupedProduct p{x, w, y, d.ldx, d.ldw, d.ldy, d.w_stride, d.R, d.E, d.N, d.K, false};
+  return hip_status(launch_grouped_rows(p, s, BM, stream));
+}
+
+int moe_grouped_matmul_grad(const moe_grouped_dims* dims, const uint16_t* dy, const uint16_t* x, const uint16_t* w,
+                            const int32_t* offsets, uint16_t* dx, void* dw, int32_t dw_dtype, int32_t accumulate,
+                            void* ws, size_t ws_bytes, hipStream_t stream) {
+  moe_grouped_dims d;
+  const int st = grouped_dims(dims, &d);
+  if (st != MOE_OK) return st;
+  if (!offsets || (!dx && !dw && d.R > 0)) return MOE_ERR_INVALID;
+  if (dw_dtype != MOE_BF16 && dw_dtype != MOE_FP32) return MOE_ERR_INVALID;
+  if (d.R > 0 && (!dy || (dx && !w) || (dw && !x))) return MOE_ERR_INVALID;
+  if (!aligned16(dy) || !aligned16(x) || !aligned16(w) || !aligned16(dx) || !aligned16(dw)) return MOE_ERR_INVALID;
+  const GroupedLayout l = grouped_layout(d);
+  if (!ws_ok(ws, ws_bytes, l.total)) return MOE_ERR_WORKSPACE;
+  const GroupedScratch s = grouped_scratch(l, ws);
+  const int BM = grouped_bm(d.R, d.E);
+  const RestRows rest{d.zero_rest ? dx : nullptr, d.lddx, d.K};
+  if (launch_grouped_tiles(offsets, d.E, (int)d.R, BM, s, rest, stream) != hipSuccess) return MOE_ERR_HIP;
+  if (dx && d.R > 0) {
+    const GroupedProduct p{dy, w, dx, d.ldy, d.ldw, d.lddx, d.w_stride, d.R, d.E, d.K, d.N, true};
+    if (launch_grouped_rows(p, s, BM, stream) != hipSuccess) return MOE_ERR_HIP;
+  }
+  if (dw) {
+    const GroupedProduct p{dy, x, dw, d.ldy, d.ldx, d.K, (int64_t)d.N * d.K, d.R, d.E, d.K, 0, true};
+    if (launch_grouped_wgrad(p, d.N, dw_dtype == MOE_FP32, accumulate != 0, s, stream) != hipSuccess)
+      return MOE_ERR_HIP;
+  }
+  return MOE_OK;
+}
+
+int moe_quantize_fp8_rows(const uint16_t* x, int64_t R, int32_t K, int64_t ldx, uint8_t* codes, float* scales,
+                          hipStream_t stream) {
+  if (R < 0 || K <= 0 || ldx < 0) return MOE_ERR_INVALID;
+  if (ldx == 0) ldx = K;
+  if (ldx < K || (R > 0 && (!x || !codes || !scales)) || !aligned16(x) || !aligned16(codes)) return MOE_ERR_INVALID;
+  if (K % 8 || ldx % 8 || R > (int64_t)0x7FFFFFFF / ((K + 127) / 128)) return MOE_ERR_UNSUPPORTED;
+  return hip_status(launch_fp8_rows(x, R, K, ldx, codes, scales, stream));
+}
+
+int moe_quantize_fp8_blocks(const uint16_t* w, int64_t count, int32_t N, int32_t K, uint8_t* codes, float* scales,
+                            hipStream_t stream) {
+  if (count < 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID;
+  if ((count > 0 && (!w || !codes || !scales)) || !aligned16(w) || !aligned16(codes)) return MOE_ERR_INVALID;
+  if (K % 8 || (int64_t)N * K > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
+  if (count > (int64_t)0x7FFFFFFF / ((int64_t)((N + 127) / 128) * ((K + 127) / 128))) return MOE_ERR_UNSUPPORTED;
+  return hip_status(launch_fp8_blocks(w, count, N, K, codes, scales, stream));
+}
+
+int moe_grouped_matmul_fp8(const moe_grouped_dims* dims, const uint8_t* xq, const float* xs, const uint8_t* wq,
+                           const float* w_scale, const int32_t* offsets, uint16_t* y, void* ws, size_t ws_bytes,
+                           hipStream_t stream) {
+  if (dims == nullptr) return MOE_ERR_INVALID;
+  moe_grouped_dims d = *dims;
+  d.ldx = d.ldw = d.w_stride = d.lddx = 0;              // codes are dense
+  const int st = grouped_dims(&d, &d);
+  if (st != MOE_OK) return st;
+  if (d.K % 16) return MOE_ERR_UNSUPPORTED;
+  if (!wq || !w_scale || !offsets || (d.R > 0 && (!xq || !xs || !y))) return MOE_ERR_INVALID;
+  if (!aligned16(xq) || !aligned16(wq) || !aligned16(y)) return MOE_ERR_INVALID;
+  const GroupedLayout l = grouped_layout(d);
+  if (!ws_ok(ws, ws_bytes, l.total)) return MOE_ERR_WORKSPACE;
+  if (d.R == 0) return MOE_OK;
+  const GroupedScratch s = grouped_scratch(l, ws);
+  const int BM = 128;
+  const RestRows rest{d.zero_rest ? y : nullptr, d.ldy, d.N};
+  if (launch_grouped_tiles(offsets, d.E, (int)d.R, BM, s, rest, stream) != hipSuccess) return MOE_ERR_HIP;
+  Fp8Args a{};
+  a.A = xq;
+  a.sx = xs;
+  a.B = wq;
+  a.sw = w_scale;
+  a.C = y;
+  a.ldc = d.ldy;
+  a.R = d.R;
+  a.N = d.N;
+  a.K = d.K;
+  a.nb = (d.N + 127) / 128;
+  a.kb = (d.K + 127) / 128;
+  a.tiles = s.tiles;
+  a.n_mtiles = s.n_mtiles;
+  a.ntiles = (d.N + 127) / 128;
+  return hip_status(launch_grouped_fp8(a, d.R, d.E, BM, stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// gradient norm and clipping
+// ---------------------------------------------------------------------------
+
+namespace {
+
+// workgroups of one launch: enough to fill the card eight deep, never more than chunks
+constexpr int kGradBlocks = 2048;
+
+size_t dtype_size(int32_t dt) { return dt == MOE_FP32 ? 4 : 2; }
+int64_t chunks_of(int64_t n) { return (n + kGradChunk - 1) / kGradChunk; }
+
+int check_tensors(const moe_grad_tensor* t, int32_t count) {
+  if (count < 0 || (count > 0 && t == nullptr)) return MOE_ERR_INVALID;
+  int64_t total = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    if (t[i].n < 0 || (t[i].dtype != MOE_BF16 && t[i].dtype != MOE_FP32)) return MOE_ERR_INVALID;
+    if (t[i].n == 0) continue;
+    const size_t sz = dtype_size(t[i].dtype);
+    if (t[i].grad == nullptr || reinterpret_cast<uintptr_t>(t[i].grad) % sz) return MOE_ERR_INVALID;
+    if (reinterpret_cast<uintptr_t>(t[i].out) % sz) return MOE_ERR_INVALID;
+    if (t[i].n > ((int64_t)1 << 40) - total) return MOE_ERR_UNSUPPORTED;
+    total += t[i].n;
+  }
+  return MOE_OK;
+}
+
+// Calls f(table, first tensor's index in order) for every launch's table of non-empty tensors.
+template <typename F>
+int for_tables(const moe_grad_tensor* t, int32_t count, F&& f) {
+  GradTable tab{};
+  auto flush = [&]() -> int {
+    if (tab.count == 0) return MOE_OK;
+    const int rc = f(tab);
+    tab = GradTable{};
+    return rc;
+  };
+  for (int32_t i = 0; i < count; ++i) {
+    if (t[i].n == 0) continue;
+    const int64_t c = chunks_of(t[i].n);             // at most 2^25
+    if (tab.count == kGradTableSize || tab.chunks + c > 0x7FFFFFFF) {
+      const int rc = flush();
+      if (rc != MOE_OK) return rc;
+    }
+    const int k = tab.count++;
+    tab.src[k] = t[i].grad;
+    tab.dst[k] = t[i].out ? t[i].out : const_cast<void*>(t[i].grad);
+    tab.n[k] = t[i].n;
+    tab.first[k] = tab.chunks;
+    if (t[i].dtype == MOE_FP32) tab.f32[k / 32] |= 1u << (k % 32);
+    tab.chunks += (int)c;
+  }
+  return flush();
+}
+
+int table_blocks(const GradTable& t) { return std::min(t.chunks, kGradBlocks); }
+
+size_t partials_of(const moe_grad_tensor* t, int32_t count) {
+  size_t n = 0;
+  for_tables(t, count, [&](const GradTable& tab) -> int { n += table_blocks(tab); return MOE_OK; });
+  return n;
+}
+
+int norm_impl(const moe_grad_tensor* t, int32_t count, double max_norm, float* norm, bool clip, void* ws,
+              size_t ws_bytes, hipStream_t stream) {
+  if (norm == nullptr) return MOE_ERR_INVALID;
+  const size_t n = partials_of(t, count);
+  if (!ws_ok(ws, ws_bytes, align_up((n + 1) * 8))) return MOE_ERR_WORKSPACE;
+  double* factor = static_cast<double*>(ws);
+  double* partial = factor + 1;
+  size_t at = 0;
+  int rc = for_tables(t, count, [&](const GradTable& tab) {
+    const int blocks = table_blocks(tab);
+    const hipError_t e = launch_grad_sumsq(tab, blocks, partial + at, stream);
+    at += blocks;
+    return hip_status(e);
+  });
+  if (rc != MOE_OK) return rc;
+  rc = hip_status(launch_grad_norm(partial, (int)n, max_norm, norm, clip ? factor : nullptr, stream));
+  if (rc != MOE_OK || !clip) return rc;
+  return for_tables(t, count, [&](const GradTable& tab) {
+    return hip_status(launch_grad_scale(tab, table_blocks(tab), factor, stream));
+  });
+}
+
+// Outputs that overlap each other, or a gradient that is not the output's own.
+bool outputs_overlap(const moe_grad_tensor* t, int32_t count) {
+  struct Span { uintptr_t lo, hi; int32_t i; bool out; };
+  std::vector<Span> v;
+  v.reserve(2 * (size_t)count);
+  for (int32_t i = 0; i < count; ++i) {
+    if (t[i].n == 0) continue;
+    const uintptr_t g = reinterpret_cast<uintptr_t>(t[i].grad), o = t[i].out ? reinterpret_cast<uintptr_t>(t[i].out) : g;
+    const uintptr_t b = (uintptr_t)t[i].n * dtype_size(t[i].dtype);
+    v.push_back({o, o + b, i, true});
+    if (o != g) v.push_back({g, g + b, i, false});
+  }
+  std::sort(v.begin(), v.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
+  // sweep: the furthest end so far of outputs and of gradients
+  uintptr_t out_hi = 0, in_hi = 0;
+  for (const Span& s : v) {
+    if (s.lo < out_hi || (s.out && s.lo < in_hi)) return true;
+    if (s.out) out_hi = std::max(out_hi, s.hi);
+    else in_hi = std::max(in_hi, s.hi);
+  }
+  return false;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t moe_grad_norm_workspace_bytes(const moe_grad_tensor* tensors, int32_t count) {
+  if (check_tensors(tensors, count) != MOE_OK) return 0;
+  return align_up((partials_of(tensors, count) + 1) * 8);
+}
+
+int moe_grad_norm(const moe_grad_tensor* tensors, int32_t count, float* norm, void* ws, size_t ws_bytes,
+                  hipStream_t stream) {
+  const int st = check_tensors(tensors, count);
+  if (st != MOE_OK) return st;
+  return norm_impl(tensors, count, 0.0, norm, false, ws, ws_bytes, stream);
+}
+
+int moe_clip_grad_norm(const moe_grad_tensor* tensors, int32_t count, float max_norm, float* norm, void* ws,
+                       size_t ws_bytes, hipStream_t stream) {
+  const int st = check_tensors(tensors, count);
+  if (st != MOE_OK) return st;
+  if (!(max_norm >= 0.f)) return MOE_ERR_INVALID;
+  try {
+    if (outputs_overlap(tensors, count)) return MOE_ERR_INVALID;
+  } catch (const std::bad_alloc&) {
+    return MOE_ERR_WORKSPACE;
+  }
+  return norm_impl(tensors, count, (double)max_norm, norm, true, ws, ws_bytes, stream);
+}
+
+}  // extern "C"
