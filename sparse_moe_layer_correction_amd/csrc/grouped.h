@@ -46,6 +46,15 @@ typedef __attribute__((address_space(3))) s16x4* lds_s16x4_ptr;
 
 constexpr uint32_t kOutOfRange = 0x80000000u;   // past every buffer range used here
 
+// The pointer as scalar registers: the compiler otherwise may keep a uniform
+// address in vector registers, and a buffer resource made of those costs a loop
+// over the lanes at every load.
+__device__ __forceinline__ const uint16_t* uniform_ptr(const uint16_t* p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((uint32_t)v), hi = __builtin_amdgcn_readfirstlane((uint32_t)(v >> 32));
+  return reinterpret_cast<const uint16_t*>(((uint64_t)hi << 32) | lo);
+}
+
 // Slot of 16-byte chunk c of reduction row k of a transposed stage of W
 // columns. A transposing read's 32 lanes take 64 bytes of each of 4 consecutive
 // rows: the four pieces have to lie in different quarters of the 256-byte bank
@@ -88,10 +97,9 @@ struct OperandLoad {
   __device__ __forceinline__ void issue(u32x4* stage, int kt, int wave) const {
     const int left = klen - kt * 64;
     if constexpr (TR) {
-      // (a scalar again: the clamp is a vector instruction, and a resource in
-      // vector registers costs a loop over the lanes at every load)
-      const int rows = __builtin_amdgcn_readfirstlane(min(max(left, 0), 64));
-      const __amdgpu_buffer_rsrc_t r = make_rsrc(base + (int64_t)(rows > 0 ? kt : 0) * 64 * ld, (int)(rows * ld * 2));
+      const int rows = min(max(left, 0), 64);
+      const __amdgpu_buffer_rsrc_t r = make_rsrc(uniform_ptr(base + (int64_t)(rows > 0 ? kt : 0) * 64 * ld),
+                                                 __builtin_amdgcn_readfirstlane((int)(rows * ld * 2)));
 #pragma unroll
       for (int i = 0; i < NL; ++i)
         __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_ptr)&stage[(wave * NL + i) * 64], 16, (int)ofs[i], 0, 0,
@@ -145,15 +153,82 @@ struct OperandRead {
   }
 };
 
-// C tile BM x BN by WM x WN waves. OUT: EPI_BF16 or EPI_F32.
-template <int FORM, int BM, int BN, int WM, int WN, int OCC, int OUT>
+// MFMA fragments of one 16-deep substep of a wave tile.
+template <int TM, int TN>
+struct GroupedFrag {
+  bf16x8 a[TM], b[TN];
+};
+
+// Epilogue of one wave's WTM x WTN tile through its staging area stg (16 KB of
+// the idle stages): a lane owns 4 consecutive columns of a row, which stored
+// directly would be 8- or 16-byte pieces of 32 rows (measured: the store
+// requests then bound the short sums of the weight gradient, 20 us a 256 x 256
+// tile); staged, every store writes whole rows of the wave tile. 16-byte chunk c
+// of row r sits at chunk c ^ (r % CPW), which spreads the 32 rows of a write
+// over the banks. dst: the wave tile's first element; rows / cols: how many of its rows
+// and columns (a multiple of 8) exist.
+template <int WTM, int WTN, int OUT>
+__device__ __forceinline__ void store_wave_tile(const f32x16 (&acc)[WTN / 32][WTM / 32], char* stg, void* dst,
+                                                int64_t ldc, int rows, int cols, bool accumulate, int lane) {
+  constexpr int ES = OUT == EPI_F32 ? 4 : 2, EPC = 16 / ES;     // bytes of an element, elements of a chunk
+  constexpr int CPW = WTN / EPC;                                // chunks of a row
+  constexpr int RP = WTM * WTN * ES <= 16384 ? WTM : 16384 / (WTN * ES);   // rows staged at a time
+  static_assert(RP % 32 == 0 && WTM % RP == 0 && 64 % CPW == 0, "staging");
+  constexpr int RPI = 64 / CPW, NRB = RP / RPI;
+#pragma unroll
+  for (int p = 0; p < WTM / RP; ++p) {
+#pragma unroll
+    for (int tm = 0; tm < RP / 32; ++tm) {
+      const int r = tm * 32 + (lane & 31);
+#pragma unroll
+      for (int tn = 0; tn < WTN / 32; ++tn)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const f32x16& v = acc[tn][p * (RP / 32) + tm];
+          if constexpr (OUT == EPI_F32) {
+            const int c = tn * 8 + g * 2 + (lane >> 5);
+            *reinterpret_cast<f32x4*>(stg + r * (CPW * 16) + ((c ^ (r % CPW)) * 16)) =
+                f32x4{v[4 * g], v[4 * g + 1], v[4 * g + 2], v[4 * g + 3]};
+          } else {
+            const int c = tn * 4 + g;
+            *reinterpret_cast<u32x2*>(stg + r * (CPW * 16) + ((c ^ (r % CPW)) * 16) + (lane >> 5) * 8) =
+                u32x2{cvt_pk_bf16(v[4 * g], v[4 * g + 1]), cvt_pk_bf16(v[4 * g + 2], v[4 * g + 3])};
+          }
+        }
+    }
+    const int r0 = lane / CPW, c = lane % CPW;
+    u32x4 rb[NRB];
+#pragma unroll
+    for (int i = 0; i < NRB; ++i) {
+      const int r = i * RPI + r0;
+      rb[i] = *reinterpret_cast<const u32x4*>(stg + r * (CPW * 16) + ((c ^ (r % CPW)) * 16));
+    }
+    const int left = rows - p * RP;
+    char* out = static_cast<char*>(dst) + ((int64_t)(p * RP + r0) * ldc + c * EPC) * ES;
+    const int64_t step = (int64_t)RPI * ldc * ES;
+    if (c * EPC < cols) {
+#pragma unroll
+      for (int i = 0; i < NRB; ++i, out += step)
+        if (i * RPI + r0 < left) {
+          u32x4 v = rb[i];
+          if constexpr (OUT == EPI_F32) {
+            if (accumulate) v = __builtin_bit_cast(u32x4, __builtin_bit_cast(f32x4, v) + *reinterpret_cast<f32x4*>(out));
+          }
+          *reinterpret_cast<u32x4*>(out) = v;
+        }
+    }
+  }
+}
+
+// C tile BM x BN by WM x WN waves. OUT: EPI_BF16 or EPI_F32. OCC: waves per
+// SIMD the registers are sized for.
+template <int FORM, int BM, int BN, int WM, int WN, int OCC, int OUT, int BST>
 __global__ void __launch_bounds__(64 * WM * WN, 1) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
 grouped_kernel(const GroupedArgs P) {
   constexpr int NT = 64 * WM * WN;
   constexpr bool AT = FORM == FORM_TN, BT = FORM != FORM_NT;
-  constexpr int WTM = BM / WM, WTN = BN / WN, TM = WTM / 32, TN = WTN / 32;
-  static_assert(TM >= 1 && TN >= 1 && BM * 8 % NT == 0 && BN * 8 % NT == 0, "tile shape");
-  __shared__ u32x4 sa0[BM * 8], sb0[BN * 8], sa1[BM * 8], sb1[BN * 8];
+  static_assert(BM * 8 % NT == 0 && BN * 8 % NT == 0, "tile shape");
+  __shared__ u32x4 sa0[BM * 8], sb0[BN * 8], sa1[BM * 8], sb1[BN * 8], sb2[BST == 3 ? BN * 8 : 1];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -168,11 +243,9 @@ grouped_kernel(const GroupedArgs P) {
     const int e = __builtin_amdgcn_readfirstlane(t / per);
     int mt, nt;
     tile_order(t - e * per, P.mtiles, P.ntiles, 4, mt, nt);
-    m0 = mt * BM;
+    m0 = __builtin_amdgcn_readfirstlane(mt * BM);
+    n0 = __builtin_amdgcn_readfirstlane(nt * BN);
     mend = P.M;
-    n0 = nt * BN;
-    m0 = __builtin_amdgcn_readfirstlane(m0);
-    n0 = __builtin_amdgcn_readfirstlane(n0);
     const int lo = __builtin_amdgcn_readfirstlane(P.ranges[e].x);
     Kd = __builtin_amdgcn_readfirstlane(P.ranges[e].y) - lo;
     if (Kd <= 0 && P.accumulate) return;
@@ -187,93 +260,184 @@ grouped_kernel(const GroupedArgs P) {
     const int e = __builtin_amdgcn_readfirstlane(rec.x), first = __builtin_amdgcn_readfirstlane(rec.y);
     const int lo = __builtin_amdgcn_readfirstlane(rec.z), hi = __builtin_amdgcn_readfirstlane(rec.w);
     int mt, nt;
-    grouped_tile_order(t - first * P.ntiles, (hi - lo + BM - 1) / BM, (hi - lo) / BM, P.ntiles, 1 << 20, mt, nt);
-    m0 = lo + mt * BM;
+    grouped_tile_order(t - first * P.ntiles, (hi - lo + BM - 1) / BM, (hi - lo) / BM, P.ntiles, 8, mt, nt);
+    m0 = __builtin_amdgcn_readfirstlane(lo + mt * BM);
+    n0 = __builtin_amdgcn_readfirstlane(nt * BN);
     mend = hi;
-    n0 = nt * BN;
-    m0 = __builtin_amdgcn_readfirstlane(m0);
-    n0 = __builtin_amdgcn_readfirstlane(n0);
     Kd = P.Kd;
     Ap = P.A + (int64_t)m0 * P.lda;
     Bp = P.B + (int64_t)e * P.b_estride + (BT ? (int64_t)n0 : (int64_t)n0 * P.ldb);
   }
 
-  OperandLoad<BM, AT, NT> la;
-  OperandLoad<BN, BT, NT> lb;
-  la.init(Ap, P.lda, mend - m0, Kd, wave, lane);
-  lb.init(Bp, P.ldb, P.N - n0, Kd, wave, lane);
-  OperandRead<BM, AT, TM> ra;
-  OperandRead<BN, BT, TN> rb;
-  ra.init(wave_m * WTM, lane);
-  rb.init(wave_n * WTN, lane);
+  // HQ: the tile's height in quarters of BM (an expert's short last tile; the
+  // weight gradient's tiles are always whole)
+  auto body = [&](auto height) __attribute__((always_inline)) {
+    constexpr int HQ = decltype(height)::value;
+    constexpr int H = BM * HQ / 4;
+    constexpr int WTM = H / WM, WTN = BN / WN, TM = WTM / 32, TN = WTN / 32;
+    static_assert(TM >= 1 && TN >= 1 && WTM % 32 == 0 && H * 8 % NT == 0, "wave tile");
+    OperandLoad<H, AT, NT> la;
+    OperandLoad<BN, BT, NT> lb;
+    la.init(Ap, P.lda, mend - m0, Kd, wave, lane);
+    lb.init(Bp, P.ldb, P.N - n0, Kd, wave, lane);
+    OperandRead<H, AT, TM> ra;
+    OperandRead<BN, BT, TN> rb;
+    ra.init(wave_m * WTM, lane);
+    rb.init(wave_n * WTN, lane);
 
-  f32x16 acc[TN][TM];
+    f32x16 acc[TN][TM];
 #pragma unroll
-  for (int a = 0; a < TN; ++a)
+    for (int a = 0; a < TN; ++a)
 #pragma unroll
-    for (int b = 0; b < TM; ++b)
+      for (int b = 0; b < TM; ++b)
 #pragma unroll
-      for (int q = 0; q < 16; ++q) acc[a][b][q] = 0.f;
+        for (int q = 0; q < 16; ++q) acc[a][b][q] = 0.f;
 
-  const int nk = (Kd + 63) / 64;
-  auto step = [&](int kt, const u32x4* a, const u32x4* b, u32x4* an, u32x4* bn) {
-    la.issue(an, kt + 1, wave);
-    lb.issue(bn, kt + 1, wave);
-#pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      bf16x8 fa[TM], fb[TN];
-      ra.read(fa, a, ks, lane);
-      rb.read(fb, b, ks, lane);
+    const int nk = (Kd + 63) / 64;
+    typedef GroupedFrag<TM, TN> Frag;
+    Frag f0, f1;
+    auto read = [&](Frag& f, const u32x4* a, const u32x4* b, int ks) {
+      ra.read(f.a, a, ks, lane);
+      rb.read(f.b, b, ks, lane);
+    };
+    auto mma = [&](const Frag& f) {
 #pragma unroll
       for (int tn = 0; tn < TN; ++tn)
 #pragma unroll
         for (int tm = 0; tm < TM; ++tm)
-          acc[tn][tm] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fb[tn], fa[tm], acc[tn][tm], 0, 0, 0);
-    }
-    MOE_WAIT_VMCNT(0);
-    __syncthreads();
-  };
-  if (nk > 0) {
-    la.issue(sa0, 0, wave);
-    lb.issue(sb0, 0, wave);
-    MOE_WAIT_VMCNT(0);
-    __syncthreads();
-    for (int kt = 0; kt < nk; kt += 2) {
-      step(kt, sa0, sb0, sa1, sb1);
-      if (kt + 1 < nk) step(kt + 1, sa1, sb1, sa0, sb0);
-    }
-  }
-
-  // lane l owns row (l & 31) of each 32 x 32 tile and columns 8 g + 4 (l >> 5) .. + 3
-#pragma unroll
-  for (int tm = 0; tm < TM; ++tm) {
-    const int m = m0 + wave_m * WTM + tm * 32 + (lane & 31);
-    if (m >= mend) continue;
-#pragma unroll
-    for (int tn = 0; tn < TN; ++tn)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int n = n0 + wave_n * WTN + tn * 32 + 8 * g + 4 * (lane >> 5);
-        if (n >= P.N) continue;
-        f32x4 v{acc[tn][tm][4 * g], acc[tn][tm][4 * g + 1], acc[tn][tm][4 * g + 2], acc[tn][tm][4 * g + 3]};
-        const int64_t at = c_base + (int64_t)m * P.ldc + n;
-        if constexpr (OUT == EPI_F32) {
-          f32x4* dst = reinterpret_cast<f32x4*>(static_cast<float*>(P.C) + at);
-          if (FORM == FORM_TN && P.accumulate) v += *dst;
-          *dst = v;
-        } else {
-          u32x2* dst = reinterpret_cast<u32x2*>(static_cast<uint16_t*>(P.C) + at);
-          if (FORM == FORM_TN && P.accumulate) {
-            const u32x2 o = *dst;
-            v[0] += bf16_bits_to_f32(o.x & 0xFFFFu);
-            v[1] += bf16_bits_to_f32(o.x >> 16);
-            v[2] += bf16_bits_to_f32(o.y & 0xFFFFu);
-            v[3] += bf16_bits_to_f32(o.y >> 16);
+          acc[tn][tm] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.b[tn], f.a[tm], acc[tn][tm], 0, 0, 0);
+    };
+    // Two LDS stages of A, BST of B. The reads of a 16-deep substep run beside
+    // the MFMAs of the one before; the one barrier of a k tile sits before its
+    // last substep, whose fragments are in registers by then: past it the next
+    // tile has landed and nobody reads this tile's stages. With three stages B
+    // is loaded two tiles ahead (the weights, which come from HBM while the
+    // rows stay in the caches), in the second substep of the tile before.
+    constexpr int NM = TM * TN, NR = TM * (AT ? 2 : 1) + TN * (BT ? 2 : 1);
+    constexpr int NA = OperandLoad<H, AT, NT>::NL, NB = OperandLoad<BN, BT, NT>::NL;
+    auto stA = [&](auto v) -> u32x4* { return decltype(v)::value == 0 ? sa0 : sa1; };
+    auto stB = [&](auto v) -> u32x4* {
+      if constexpr (decltype(v)::value == 0) return sb0;
+      else if constexpr (decltype(v)::value == 1) return sb1;
+      else return sb2;
+    };
+    // s_waitcnt vmcnt(BST == 3 ? NB : 0) lgkmcnt(0): with three stages the loads of B tile kt + 2 stay in flight
+    constexpr int VM = BST == 3 ? NB : 0;
+    constexpr int kWait = (VM & 0xF) | (0x7 << 4) | (0x0 << 8) | (((VM >> 4) & 3) << 14);
+    auto step = [&](int kt, auto sa, auto sb, auto first) {
+      constexpr int SA = decltype(sa)::value, SB = decltype(sb)::value;
+      constexpr bool MID = BST == 3 && decltype(first)::value == 0;   // tile 2 was loaded before step 0
+      read(f1, stA(sa), stB(sb), 1);
+      mma(f0);
+      interleave<NM, NR, 0>();
+      read(f0, stA(sa), stB(sb), 2);
+      if constexpr (MID) lb.issue(stB(Stage<(SB + 2) % 3>{}), kt + 2, wave);
+      mma(f1);
+      interleave<NM, NR, MID ? NB : 0>();
+      read(f1, stA(sa), stB(sb), 3);
+      mma(f0);
+      interleave<NM, NR, 0>();
+      __builtin_amdgcn_s_waitcnt(kWait);
+      asm volatile("s_barrier" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      la.issue(stA(sa), kt + 2, wave);
+      if constexpr (BST == 2) lb.issue(stB(sb), kt + 2, wave);
+      read(f0, stA(Stage<1 - SA>{}), stB(Stage<(SB + 1) % BST>{}), 0);
+      mma(f1);
+      interleave<NM, NR, NA + (BST == 2 ? NB : 0)>();
+    };
+    if (nk > 0) {
+      la.issue(sa0, 0, wave);
+      lb.issue(sb0, 0, wave);
+      la.issue(sa1, 1, wave);
+      lb.issue(sb1, 1, wave);
+      if constexpr (BST == 3) lb.issue(sb2, 2, wave);
+      MOE_WAIT_VMCNT(NA + (BST - 1) * NB);
+      asm volatile("s_barrier" ::: "memory");
+      __builtin_amdgcn_sched_barrier(0);
+      read(f0, sa0, sb0, 0);
+      const Stage<0> S0{};
+      const Stage<1> S1{};
+      const Stage<2> S2{};
+      if constexpr (BST == 2) {
+        int kt = 0;
+        for (; kt + 1 < nk; kt += 2) {
+          step(kt, S0, S0, S0);
+          step(kt + 1, S1, S1, S0);
+        }
+        if (kt < nk) step(kt, S0, S0, S0);
+      } else {
+        step(0, S0, S0, S1);
+        // step kt reads A stage kt % 2 and B stage kt % 3
+        int kt = 1;
+        for (; kt + 6 <= nk; kt += 6) {
+          step(kt, S1, S1, S0);
+          step(kt + 1, S0, S2, S0);
+          step(kt + 2, S1, S0, S0);
+          step(kt + 3, S0, S1, S0);
+          step(kt + 4, S1, S2, S0);
+          step(kt + 5, S0, S0, S0);
+        }
+        if (kt < nk) {
+          step(kt, S1, S1, S0);
+          if (kt + 1 < nk) {
+            step(kt + 1, S0, S2, S0);
+            if (kt + 2 < nk) {
+              step(kt + 2, S1, S0, S0);
+              if (kt + 3 < nk) {
+                step(kt + 3, S0, S1, S0);
+                if (kt + 4 < nk) step(kt + 4, S1, S2, S0);
+              }
+            }
           }
-          *dst = u32x2{cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
         }
       }
+    }
+    MOE_WAIT_VMCNT(0);   // no load may write a stage that the epilogue uses, or that the next workgroup gets
+    __syncthreads();
+    // 16 KB of staging per wave: an array each, or half of one
+    constexpr int per = BM * 8 * 16 / 16384;
+    static_assert(WM * WN <= 4 * per, "staging areas");
+    const int h = wave / per;
+    char* stg = reinterpret_cast<char*>(h == 0 ? sa0 : h == 1 ? sb0 : h == 2 ? sa1 : sb1) + (wave % per) * 16384;
+    const int mw = m0 + wave_m * WTM, nw = n0 + wave_n * WTN;
+    constexpr int ES = OUT == EPI_F32 ? 4 : 2;
+    void* dst = static_cast<char*>(P.C) + (c_base + (int64_t)mw * P.ldc + nw) * ES;
+    bool add = false;
+    if constexpr (FORM == FORM_TN) {
+      add = P.accumulate != 0;
+      if constexpr (OUT == EPI_BF16) {
+        // bf16 sums are added in fp32, before the one rounding
+        if (add) {
+#pragma unroll
+          for (int tm = 0; tm < TM; ++tm) {
+            const int r = tm * 32 + (lane & 31);
+#pragma unroll
+            for (int tn = 0; tn < TN; ++tn)
+#pragma unroll
+              for (int g = 0; g < 4; ++g) {
+                const int c = tn * 32 + 8 * g + 4 * (lane >> 5);
+                if (mw + r >= mend || nw + c >= P.N) continue;
+                const u32x2 o = *reinterpret_cast<const u32x2*>(static_cast<const uint16_t*>(dst) + (int64_t)r * P.ldc + c);
+                acc[tn][tm][4 * g] += bf16_bits_to_f32(o.x & 0xFFFFu);
+                acc[tn][tm][4 * g + 1] += bf16_bits_to_f32(o.x >> 16);
+                acc[tn][tm][4 * g + 2] += bf16_bits_to_f32(o.y & 0xFFFFu);
+                acc[tn][tm][4 * g + 3] += bf16_bits_to_f32(o.y >> 16);
+              }
+          }
+        }
+      }
+    }
+    store_wave_tile<WTM, WTN, OUT>(acc, stg, dst, P.ldc, mend - mw, P.N - nw, add, lane);
+  };
+  if constexpr (FORM != FORM_TN && BM == 256) {
+    // an expert's short last tile at a quarter, half or three quarters of the height
+    const int rows = mend - m0;
+    if (rows <= 64) { body(Stage<1>{}); return; }
+    if (rows <= 128) { body(Stage<2>{}); return; }
+    if (rows <= 192) { body(Stage<3>{}); return; }
   }
+  body(Stage<4>{});
 }
 
 }  // namespace moe

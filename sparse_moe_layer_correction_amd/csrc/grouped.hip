@@ -66,12 +66,25 @@ hipError_t launch_grouped_tiles(const int32_t* offsets, int E, int R, int BM, co
   return hipGetLastError();
 }
 
+#ifndef GT_BIG
+#define GT_BIG 2
+#endif
+#ifndef GT_BST
+#define GT_BST 3
+#endif
 template <int FORM, int OUT>
-static void launch_form(const GroupedArgs& a, int64_t grid, hipStream_t st) {
-  hipLaunchKernelGGL((grouped_kernel<FORM, 128, 128, 2, 2, 2, OUT>), dim3((unsigned)grid), dim3(256), 0, st, a);
+static void launch_form(const GroupedArgs& a, int BM, int64_t grid, hipStream_t st) {
+  if (BM == 256) {
+#if GT_BIG == 1
+    hipLaunchKernelGGL((grouped_kernel<FORM, 256, 256, 2, 2, 1, OUT, GT_BST>), dim3((unsigned)grid), dim3(256), 0, st, a);
+#else
+    hipLaunchKernelGGL((grouped_kernel<FORM, 256, 256, 2, 4, 2, OUT, GT_BST>), dim3((unsigned)grid), dim3(512), 0, st, a);
+#endif
+  } else
+    hipLaunchKernelGGL((grouped_kernel<FORM, 128, 128, 2, 2, 2, OUT, 2>), dim3((unsigned)grid), dim3(256), 0, st, a);
 }
 
-int grouped_bm(int64_t R, int E) { (void)R; (void)E; return 128; }
+int grouped_bm(int64_t R, int E) { return R >= (int64_t)E * 128 ? 256 : 128; }
 
 hipError_t launch_grouped_rows(const GroupedProduct& p, const GroupedScratch& s, int BM, hipStream_t st) {
   GroupedArgs a{};
@@ -86,11 +99,11 @@ hipError_t launch_grouped_rows(const GroupedProduct& p, const GroupedScratch& s,
   a.Kd = p.Kd;
   a.tiles = s.tiles;
   a.n_mtiles = s.n_mtiles;
-  a.ntiles = (p.N + 127) / 128;
+  a.ntiles = (p.N + BM - 1) / BM;
   const int64_t grid = grouped_max_tiles(p.R, p.E, BM) * a.ntiles;
   if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-  if (p.transposed_b) launch_form<FORM_NN, EPI_BF16>(a, grid, st);
-  else launch_form<FORM_NT, EPI_BF16>(a, grid, st);
+  if (p.transposed_b) launch_form<FORM_NN, EPI_BF16>(a, BM, grid, st);
+  else launch_form<FORM_NT, EPI_BF16>(a, BM, grid, st);
   return hipGetLastError();
 }
 
@@ -107,13 +120,17 @@ hipError_t launch_grouped_wgrad(const GroupedProduct& p, int M, bool f32, bool a
   a.M = M;
   a.N = p.N;
   a.ranges = s.ranges;
-  a.mtiles = (M + 127) / 128;
-  a.ntiles = (p.N + 127) / 128;
+#ifndef WG_BM
+#define WG_BM ((int64_t)p.E * ((M + 255) / 256) * ((p.N + 255) / 256) >= 256 ? 256 : 128)
+#endif
+  const int BM = WG_BM;
+  a.mtiles = (M + BM - 1) / BM;
+  a.ntiles = (p.N + BM - 1) / BM;
   a.accumulate = accumulate;
   const int64_t grid = (int64_t)p.E * a.mtiles * a.ntiles;
   if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-  if (f32) launch_form<FORM_TN, EPI_F32>(a, grid, st);
-  else launch_form<FORM_TN, EPI_BF16>(a, grid, st);
+  if (f32) launch_form<FORM_TN, EPI_F32>(a, BM, grid, st);
+  else launch_form<FORM_TN, EPI_BF16>(a, BM, grid, st);
   return hipGetLastError();
 }
 
