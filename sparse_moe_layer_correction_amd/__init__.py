@@ -544,79 +544,87 @@ def bias_update(offsets, corr_bias, eta: float, *, stream=None):
 # the experts' products on their own, their gradients, 8-bit experts
 # ----------------------------------------------------------------------------
 
-class _on:
-    """Makes ``device`` current and allocates on ``stream`` (default: the device's current
-    stream), so that scratch freed on return is reused in that stream's order."""
-
-    def __init__(self, device, stream):
-        torch = _torch()
-        if device.type != "cuda":
-            raise ValueError(f"tensors must be on the GPU, got {device}")
-        if stream is not None and stream.device != device:
+def _elsewhere(device, stream):
+    """None if a call on tensors of ``device`` can go straight to the current stream; else the
+    context to make it in (``stream`` current, or the tensors' device), so that what it
+    allocates is reused in that stream's order."""
+    torch = _torch()
+    if device.type != "cuda":
+        raise ValueError(f"tensors must be on the GPU, got {device}")
+    if stream is not None:
+        if stream.device != device:
             raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
-        self._ctx = torch.cuda.device(device) if stream is None else torch.cuda.stream(stream)
-        self._device = device
-        self._given = stream
-
-    def __enter__(self):
-        self._ctx.__enter__()
-        s = self._given if self._given is not None else _torch().cuda.current_stream(self._device)
-        return s.cuda_stream
-
-    def __exit__(self, *exc):
-        return self._ctx.__exit__(*exc)
+        return torch.cuda.stream(stream)
+    return None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
 
 
-def _need_rows(t, name, dtype, shape, device):
+def _raw_stream(device) -> int:
+    # (torch.cuda.current_stream wraps the same handle in a Stream object: 2 us a call)
+    return _torch()._C._cuda_getCurrentRawStream(device.index)
+
+
+def _need_rows(t, name, dtype, rows, cols, device):
     """A matrix [rows, cols] whose columns are contiguous; returns its row stride."""
     torch = _torch()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dtype != dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
+    if t.shape != (rows, cols):
+        raise ValueError(f"{name} must have shape {(rows, cols)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on the GPU device {device}")
-    if shape[0] <= 1:
-        if shape[1] > 1 and t.stride(1) != 1 and t.numel():
-            raise ValueError(f"{name}'s columns must be contiguous")
-        return shape[1]
-    if (shape[1] > 1 and t.stride(1) != 1) or t.stride(0) < shape[1]:
-        raise ValueError(f"{name} must have contiguous columns and a row stride of at least {shape[1]}, "
-                         f"got strides {tuple(t.stride())}")
-    return t.stride(0)
+    rs, cs = t.stride()
+    if cols > 1 and cs != 1 and rows:
+        raise ValueError(f"{name}'s columns must be contiguous, got strides {(rs, cs)}")
+    if rows <= 1:
+        return cols
+    if rs < cols:
+        raise ValueError(f"{name} must have a row stride of at least {cols}, got strides {(rs, cs)}")
+    return rs
 
 
-def _grouped_shapes(x, w, offsets):
+def _need_weight(w, offsets, dtype, device):
+    """w [E, N, K] and offsets [E+1]; returns E, N, K, the row and the expert stride."""
     torch = _torch()
-    for t, name, nd in ((x, "x", 2), (w, "w", 3), (offsets, "offsets", 1)):
-        if not isinstance(t, torch.Tensor):
-            raise TypeError(f"{name} must be a torch tensor")
-        if t.dim() != nd:
-            raise ValueError(f"{name} must have {nd} dimensions, got shape {tuple(t.shape)}")
+    if not isinstance(w, torch.Tensor) or not isinstance(offsets, torch.Tensor):
+        raise TypeError("w and offsets must be torch tensors")
+    if w.dim() != 3:
+        raise ValueError(f"w must have 3 dimensions, got shape {tuple(w.shape)}")
     E, N, K = w.shape
-    _need(offsets, "offsets", torch.int32, (E + 1,), w.device)
-    return E, N, K
-
-
-def _weight_strides(w, dtype, device):
-    """Row and expert strides of w [E, N, K]."""
-    E, N, K = w.shape
-    if w.dtype != dtype:
-        raise TypeError(f"w must be {dtype}, got {w.dtype}")
-    if w.device != device:
-        raise ValueError(f"w must be on the GPU device {device}")
-    ldw = w.stride(1) if N > 1 else K
-    es = w.stride(0) if E > 1 else N * ldw
-    if (K > 1 and w.stride(2) != 1) or ldw < K or es < (N - 1) * ldw + K:
+    if w.dtype != dtype or offsets.dtype != torch.int32:
+        raise TypeError(f"w must be {dtype} and offsets int32, got {w.dtype} and {offsets.dtype}")
+    if w.device != device or offsets.device != device:
+        raise ValueError(f"w and offsets must be on the GPU device {device}")
+    if offsets.shape != (E + 1,) or (E and offsets.stride(0) != 1):
+        raise ValueError(f"offsets must be contiguous of shape {(E + 1,)}, got {tuple(offsets.shape)}")
+    es, ldw, ks = w.stride()
+    if N <= 1:
+        ldw = K
+    if E <= 1:
+        es = N * ldw
+    if (K > 1 and ks != 1) or ldw < K or es < (N - 1) * ldw + K:
         raise ValueError(f"w must hold separate [N, K] matrices with contiguous rows, got strides {tuple(w.stride())}")
-    return ldw, es
+    return E, N, K, ldw, es
 
 
-def _grouped_ws(d: _GroupedDims, device, ws):
-    nbytes = load_library().moe_grouped_workspace_bytes(ctypes.byref(d))
-    return _workspace(nbytes, device, ws)
+def _need_matrix(t, name):
+    torch = _torch()
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch tensor")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions, got shape {tuple(t.shape)}")
+
+
+def _grouped_ws(lib, d: _GroupedDims, device, ws):
+    """The workspace's address and size (and the tensor, which the caller keeps until the launch)."""
+    if ws is None:
+        nbytes = lib.moe_grouped_workspace_bytes(ctypes.byref(d))
+        ws = _torch().empty(max(nbytes, 1), dtype=_torch().uint8, device=device)
+        return ws, nbytes
+    if ws.device != device:
+        raise ValueError(f"ws must be on the GPU device {device}")
+    return ws, ws.numel() * ws.element_size()
 
 
 def grouped_workspace_bytes(R: int, E: int, N: int, K: int) -> int:
@@ -628,22 +636,29 @@ def grouped_matmul(x, w, offsets, *, out=None, ws=None, stream=None):
     """moe_grouped_matmul: y[r] = x[r] . w[e]^T for the rows offsets[e] <= r < offsets[e+1].
 
     x [R, K] and w [E, N, K] bf16 (rows contiguous, strides multiples of 8), offsets [E+1]
-    int32 on the device (``permute``, or the forward's). Returns y [R, N] bf16; rows that
+    int32 on the device (``permute``'s, or the forward's). Returns y [R, N] bf16; rows that
     belong to no expert are left as they are in ``out`` (zero when it is not given)."""
     torch = _torch()
-    E, N, K = _grouped_shapes(x, w, offsets)
-    R, dev = x.shape[0], x.device
-    ldx = _need_rows(x, "x", torch.bfloat16, (R, K), dev)
-    ldw, es = _weight_strides(w, torch.bfloat16, dev)
-    with _on(dev, stream) as st:
-        fresh = out is None
-        if fresh:
-            out = torch.empty(R, N, dtype=torch.bfloat16, device=dev)
-        ldy = _need_rows(out, "out", torch.bfloat16, (R, N), dev)
-        d = _GroupedDims(R, E, N, K, ldx, ldy, ldw, es, 0, int(fresh))
-        wsp = _grouped_ws(d, dev, ws)
-        _check(load_library().moe_grouped_matmul(ctypes.byref(d), _ptr(x), _ptr(w), _ptr(offsets), _ptr(out),
-                                                 _ptr(wsp), wsp.numel() * wsp.element_size(), st))
+    _need_matrix(x, "x")
+    dev = x.device
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return grouped_matmul(x, w, offsets, out=out, ws=ws)
+    E, N, K, ldw, es = _need_weight(w, offsets, torch.bfloat16, dev)
+    R = x.shape[0]
+    ldx = _need_rows(x, "x", torch.bfloat16, R, K, dev)
+    fresh = out is None
+    if fresh:
+        out = torch.empty(R, N, dtype=torch.bfloat16, device=dev)
+        ldy = N
+    else:
+        ldy = _need_rows(out, "out", torch.bfloat16, R, N, dev)
+    lib = load_library()
+    d = _GroupedDims(R, E, N, K, ldx, ldy, ldw, es, 0, fresh)
+    ws, nbytes = _grouped_ws(lib, d, dev, ws)
+    _check(lib.moe_grouped_matmul(ctypes.byref(d), x.data_ptr(), w.data_ptr(), offsets.data_ptr(), out.data_ptr(),
+                                  ws.data_ptr(), nbytes, _raw_stream(dev)))
     return out
 
 
@@ -655,13 +670,18 @@ def grouped_matmul_grad(dy, x, w, offsets, *, need_dx: bool = True, need_dw: boo
     ``dw_dtype`` (bf16 by default, or fp32), zero for experts without rows. ``accumulate``
     adds to the ``dw`` given. need_dx / need_dw False: that gradient is not computed (None)."""
     torch = _torch()
-    E, N, K = _grouped_shapes(x, w, offsets)
-    R, dev = x.shape[0], x.device
-    ldx = _need_rows(x, "x", torch.bfloat16, (R, K), dev)
-    if not isinstance(dy, torch.Tensor) or dy.dim() != 2:
-        raise TypeError("dy must be a [R, N] torch tensor")
-    ldy = _need_rows(dy, "dy", torch.bfloat16, (R, N), dev)
-    ldw, es = _weight_strides(w, torch.bfloat16, dev)
+    _need_matrix(x, "x")
+    _need_matrix(dy, "dy")
+    dev = x.device
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return grouped_matmul_grad(dy, x, w, offsets, need_dx=need_dx, need_dw=need_dw, dx=dx, dw=dw,
+                                       dw_dtype=dw_dtype, accumulate=accumulate, ws=ws)
+    E, N, K, ldw, es = _need_weight(w, offsets, torch.bfloat16, dev)
+    R = x.shape[0]
+    ldx = _need_rows(x, "x", torch.bfloat16, R, K, dev)
+    ldy = _need_rows(dy, "dy", torch.bfloat16, R, N, dev)
     if not (need_dx or need_dw):
         raise ValueError("one of need_dx and need_dw must be set")
     if accumulate and (dw is None or not need_dw):
@@ -670,36 +690,43 @@ def grouped_matmul_grad(dy, x, w, offsets, *, need_dx: bool = True, need_dw: boo
         dw_dtype = dw.dtype if dw is not None else torch.bfloat16
     if dw_dtype not in (torch.bfloat16, torch.float32):
         raise TypeError(f"dw_dtype must be bfloat16 or float32, got {dw_dtype}")
-    with _on(dev, stream) as st:
-        lddx, fresh = 0, dx is None
-        if need_dx:
-            if fresh:
-                dx = torch.empty(R, K, dtype=torch.bfloat16, device=dev)
-            lddx = _need_rows(dx, "dx", torch.bfloat16, (R, K), dev)
-        if need_dw:
-            if dw is None:
-                dw = torch.empty(E, N, K, dtype=dw_dtype, device=dev)
-            _need(dw, "dw", dw_dtype, (E, N, K), dev)
-        d = _GroupedDims(R, E, N, K, ldx, ldy, ldw, es, lddx, int(fresh))
-        wsp = _grouped_ws(d, dev, ws)
-        _check(load_library().moe_grouped_matmul_grad(
-            ctypes.byref(d), _ptr(dy), _ptr(x), _ptr(w), _ptr(offsets), _ptr(dx) if need_dx else None,
-            _ptr(dw) if need_dw else None, 1 if dw_dtype == torch.float32 else 0, int(accumulate), _ptr(wsp),
-            wsp.numel() * wsp.element_size(), st))
-    return (dx if need_dx else None), (dw if need_dw else None)
+    lddx, fresh = 0, dx is None
+    if not need_dx:
+        dx = None
+    elif fresh:
+        dx = torch.empty(R, K, dtype=torch.bfloat16, device=dev)
+    else:
+        lddx = _need_rows(dx, "dx", torch.bfloat16, R, K, dev)
+    if not need_dw:
+        dw = None
+    elif dw is None:
+        dw = torch.empty(E, N, K, dtype=dw_dtype, device=dev)
+    else:
+        _need(dw, "dw", dw_dtype, (E, N, K), dev)
+    lib = load_library()
+    d = _GroupedDims(R, E, N, K, ldx, ldy, ldw, es, lddx, fresh)
+    ws, nbytes = _grouped_ws(lib, d, dev, ws)
+    _check(lib.moe_grouped_matmul_grad(ctypes.byref(d), dy.data_ptr(), x.data_ptr(), w.data_ptr(), offsets.data_ptr(),
+                                       _ptr(dx), _ptr(dw), dw_dtype == torch.float32, accumulate, ws.data_ptr(),
+                                       nbytes, _raw_stream(dev)))
+    return dx, dw
 
 
 def quantize_fp8_rows(x, *, stream=None):
     """moe_quantize_fp8_rows: x [R, K] bf16 -> (codes uint8 [R, K], scales fp32 [ceil(K/128), R])."""
     torch = _torch()
-    if not isinstance(x, torch.Tensor) or x.dim() != 2:
-        raise TypeError("x must be a [R, K] torch tensor")
+    _need_matrix(x, "x")
+    dev = x.device
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return quantize_fp8_rows(x)
     R, K = x.shape
-    ldx = _need_rows(x, "x", torch.bfloat16, (R, K), x.device)
-    with _on(x.device, stream) as st:
-        codes = torch.empty(R, K, dtype=torch.uint8, device=x.device)
-        scales = torch.empty((K + 127) // 128, R, dtype=torch.float32, device=x.device)
-        _check(load_library().moe_quantize_fp8_rows(_ptr(x), R, K, ldx, _ptr(codes), _ptr(scales), st))
+    ldx = _need_rows(x, "x", torch.bfloat16, R, K, dev)
+    codes = torch.empty(R, K, dtype=torch.uint8, device=dev)
+    scales = torch.empty((K + 127) // 128, R, dtype=torch.float32, device=dev)
+    _check(load_library().moe_quantize_fp8_rows(x.data_ptr(), R, K, ldx, codes.data_ptr(), scales.data_ptr(),
+                                                _raw_stream(dev)))
     return codes, scales
 
 
@@ -709,14 +736,18 @@ def quantize_fp8_blocks(w, *, stream=None):
     torch = _torch()
     if not isinstance(w, torch.Tensor) or w.dim() < 2 or w.dtype != torch.bfloat16:
         raise TypeError("w must be a [..., N, K] bf16 torch tensor")
-    _need(w, "w", torch.bfloat16, w.shape, w.device)
+    dev = w.device
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return quantize_fp8_blocks(w)
+    _need(w, "w", torch.bfloat16, w.shape, dev)
     N, K = w.shape[-2:]
     count = w.numel() // (N * K) if N * K else 0
-    with _on(w.device, stream) as st:
-        codes = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
-        scales = torch.empty(w.shape[:-2] + ((N + 127) // 128, (K + 127) // 128), dtype=torch.float32,
-                             device=w.device)
-        _check(load_library().moe_quantize_fp8_blocks(_ptr(w), count, N, K, _ptr(codes), _ptr(scales), st))
+    codes = torch.empty(w.shape, dtype=torch.uint8, device=dev)
+    scales = torch.empty(w.shape[:-2] + ((N + 127) // 128, (K + 127) // 128), dtype=torch.float32, device=dev)
+    _check(load_library().moe_quantize_fp8_blocks(w.data_ptr(), count, N, K, codes.data_ptr(), scales.data_ptr(),
+                                                  _raw_stream(dev)))
     return codes, scales
 
 
@@ -725,30 +756,40 @@ def grouped_matmul_fp8(x, w_codes, w_scale, offsets, *, x_scale=None, out=None, 
     codes [E, N, K] with any fp32 scales [E, ceil(N/128), ceil(K/128)]).
 
     x: [R, K] bf16, quantised here (``quantize_fp8_rows``), or its codes with ``x_scale``
-    given. K a multiple of 16. Returns y [R, N] bf16."""
+    given. K a multiple of 16. Returns y [R, N] bf16 (rows without an expert as in
+    ``grouped_matmul``)."""
     torch = _torch()
-    E, N, K = _grouped_shapes(x, w_codes, offsets)
-    R, dev = x.shape[0], x.device
+    _need_matrix(x, "x")
+    dev = x.device
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return grouped_matmul_fp8(x, w_codes, w_scale, offsets, x_scale=x_scale, out=out, ws=ws)
+    E, N, K, ldw, es = _need_weight(w_codes, offsets, torch.uint8, dev)
+    R = x.shape[0]
     kb, nb = (K + 127) // 128, (N + 127) // 128
-    _need(w_codes, "w_codes", torch.uint8, (E, N, K), dev)
+    if not w_codes.is_contiguous():
+        raise ValueError("w_codes must be contiguous")
     _need(w_scale, "w_scale", torch.float32, (E, nb, kb), dev)
     if x_scale is None:
-        _need_rows(x, "x", torch.bfloat16, (R, K), dev)
+        _need_rows(x, "x", torch.bfloat16, R, K, dev)
     else:
         _need(x, "x", torch.uint8, (R, K), dev)
         _need(x_scale, "x_scale", torch.float32, (kb, R), dev)
-    with _on(dev, stream) as st:
-        fresh = out is None
-        if fresh:
-            out = torch.empty(R, N, dtype=torch.bfloat16, device=dev)
-        ldy = _need_rows(out, "out", torch.bfloat16, (R, N), dev)
-        if x_scale is None:
-            x, x_scale = quantize_fp8_rows(x, stream=stream)
-        d = _GroupedDims(R, E, N, K, 0, ldy, 0, 0, 0, int(fresh))
-        wsp = _grouped_ws(d, dev, ws)
-        _check(load_library().moe_grouped_matmul_fp8(ctypes.byref(d), _ptr(x), _ptr(x_scale), _ptr(w_codes),
-                                                     _ptr(w_scale), _ptr(offsets), _ptr(out), _ptr(wsp),
-                                                     wsp.numel() * wsp.element_size(), st))
+    fresh = out is None
+    if fresh:
+        out = torch.empty(R, N, dtype=torch.bfloat16, device=dev)
+        ldy = N
+    else:
+        ldy = _need_rows(out, "out", torch.bfloat16, R, N, dev)
+    if x_scale is None:
+        x, x_scale = quantize_fp8_rows(x)
+    lib = load_library()
+    d = _GroupedDims(R, E, N, K, 0, ldy, 0, 0, 0, fresh)
+    ws, nbytes = _grouped_ws(lib, d, dev, ws)
+    _check(lib.moe_grouped_matmul_fp8(ctypes.byref(d), x.data_ptr(), x_scale.data_ptr(), w_codes.data_ptr(),
+                                      w_scale.data_ptr(), offsets.data_ptr(), out.data_ptr(), ws.data_ptr(), nbytes,
+                                      _raw_stream(dev)))
     return out
 
 
@@ -757,45 +798,59 @@ def grouped_matmul_fp8(x, w_codes, w_scale, offsets, *, x_scale=None, out=None, 
 # ----------------------------------------------------------------------------
 
 def _grad_table(grads, out):
+    """The moe_grad_tensor array of ``grads`` (and their number and device)."""
     torch = _torch()
     grads = list(grads)
-    out = None if out is None else list(out)
-    if out is not None and len(out) != len(grads):
-        raise ValueError(f"out must hold one tensor for each of the {len(grads)} gradients, got {len(out)}")
+    outs = grads if out is None else list(out)
+    if len(outs) != len(grads):
+        raise ValueError(f"out must hold one tensor for each of the {len(grads)} gradients, got {len(outs)}")
     if not grads:
         raise ValueError("grads must hold at least one tensor")
-    dev = grads[0].device if isinstance(grads[0], torch.Tensor) else None
     kinds = {torch.bfloat16: 0, torch.float32: 1}
-    tab = (_GradTensor * len(grads))()
-    for i, g in enumerate(grads):
+    index = grads[0].get_device() if isinstance(grads[0], torch.Tensor) else -1
+    words = []                       # four 64-bit words an entry: grad, out, n, dtype (and its padding)
+    for i, (g, o) in enumerate(zip(grads, outs)):
         if not isinstance(g, torch.Tensor) or g.dtype not in kinds:
             raise TypeError(f"gradient {i} must be a bf16 or fp32 torch tensor")
-        if g.device != dev or not g.is_cuda:
-            raise ValueError(f"gradient {i} must be on the GPU device {dev}")
+        if index < 0 or g.get_device() != index:
+            raise ValueError(f"gradient {i} must be on the GPU of the first one, got {g.device}")
         if not g.is_contiguous():
             raise ValueError(f"gradient {i} must be contiguous")
-        o = None
-        if out is not None:
-            o = out[i]
-            if not isinstance(o, torch.Tensor) or o.dtype != g.dtype or o.shape != g.shape or o.device != dev \
-                    or not o.is_contiguous():
-                raise ValueError(f"out {i} must be a contiguous {g.dtype} tensor of shape {tuple(g.shape)} on {dev}")
-        e = tab[i]
-        e.grad, e.out, e.n, e.dtype = g.data_ptr(), None if o is None else o.data_ptr(), g.numel(), kinds[g.dtype]
-    return tab, len(grads), dev
+        n, at = g.numel(), g.data_ptr()
+        if o is g:
+            words += (at, 0, n, kinds[g.dtype])
+            continue
+        if not isinstance(o, torch.Tensor) or o.dtype != g.dtype or o.numel() != n or o.get_device() != index \
+                or not o.is_contiguous():
+            raise ValueError(f"out {i} must be a contiguous {g.dtype} tensor of {n} elements on {g.device}")
+        words += (at, o.data_ptr(), n, kinds[g.dtype])
+    raw = (ctypes.c_int64 * len(words))(*words)
+    return ctypes.cast(raw, ctypes.POINTER(_GradTensor)), raw, len(grads), grads[0].device
+
+
+def _grad_ws(lib, tab, n, device, ws):
+    if ws is not None:
+        if ws.device != device:
+            raise ValueError(f"ws must be on the GPU device {device}")
+        return ws, ws.numel() * ws.element_size()
+    nbytes = lib.moe_grad_norm_workspace_bytes(tab, n)
+    return _torch().empty(max(nbytes, 1), dtype=_torch().uint8, device=device), nbytes
 
 
 def grad_norm(grads, *, ws=None, stream=None):
     """moe_grad_norm: sqrt of the sum of squares over all ``grads`` (bf16 and fp32 tensors on one
     GPU, contiguous) as a 0-dimensional fp32 tensor on that GPU."""
     torch = _torch()
-    tab, n, dev = _grad_table(grads, None)
+    grads = list(grads)
+    tab, _keep, n, dev = _grad_table(grads, None)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return grad_norm(grads, ws=ws)
     lib = load_library()
-    with _on(dev, stream) as st:
-        norm = torch.empty((), dtype=torch.float32, device=dev)
-        nbytes = lib.moe_grad_norm_workspace_bytes(tab, n)
-        w = _workspace(nbytes, dev, ws)
-        _check(lib.moe_grad_norm(tab, n, _ptr(norm), _ptr(w), w.numel() * w.element_size(), st))
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    ws, nbytes = _grad_ws(lib, tab, n, dev, ws)
+    _check(lib.moe_grad_norm(tab, n, norm.data_ptr(), ws.data_ptr(), nbytes, _raw_stream(dev)))
     return norm
 
 
@@ -804,13 +859,17 @@ def clip_grad_norm(grads, max_norm: float, *, out=None, ws=None, stream=None):
     above max_norm, in place or into ``out`` (one tensor for each). Returns the norm before the
     clip as a 0-dimensional fp32 tensor on the GPU; nothing waits for it."""
     torch = _torch()
-    tab, n, dev = _grad_table(grads, out)
+    grads = list(grads)
+    out = None if out is None else list(out)
+    tab, _keep, n, dev = _grad_table(grads, out)
+    ctx = _elsewhere(dev, stream)
+    if ctx is not None:
+        with ctx:
+            return clip_grad_norm(grads, max_norm, out=out, ws=ws)
     lib = load_library()
-    with _on(dev, stream) as st:
-        norm = torch.empty((), dtype=torch.float32, device=dev)
-        nbytes = lib.moe_grad_norm_workspace_bytes(tab, n)
-        w = _workspace(nbytes, dev, ws)
-        _check(lib.moe_clip_grad_norm(tab, n, max_norm, _ptr(norm), _ptr(w), w.numel() * w.element_size(), st))
+    norm = torch.empty((), dtype=torch.float32, device=dev)
+    ws, nbytes = _grad_ws(lib, tab, n, dev, ws)
+    _check(lib.moe_clip_grad_norm(tab, n, max_norm, norm.data_ptr(), ws.data_ptr(), nbytes, _raw_stream(dev)))
     return norm
 
 

@@ -143,10 +143,23 @@ hipError_t launch_fp8_blocks(const uint16_t* w, int64_t count, int N, int K, uin
   return hipGetLastError();
 }
 
-hipError_t launch_grouped_fp8(const Fp8Args& a, int64_t R, int E, int BM, hipStream_t st) {
-  const int64_t grid = grouped_max_tiles(R, E, BM) * a.ntiles;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-  hipLaunchKernelGGL((grouped_fp8_kernel<128, 128, 2, 2, 2>), dim3((unsigned)grid), dim3(256), 0, st, a);
+GroupedPlan fp8_plan(int64_t R, int E, int N) {
+  GroupedPlan p;
+  p.bm = R >= (int64_t)E * 128 ? 256 : 128;
+  p.mtiles = 0;
+  p.ntiles = (N + p.bm - 1) / p.bm;
+  p.grid = grouped_max_tiles(R, E, p.bm) * p.ntiles;
+  p.scan = p.grid <= 1024 && E <= 128;
+  return p;
+}
+
+hipError_t launch_grouped_fp8(const Fp8Args& a, const GroupedPlan& plan, hipStream_t st) {
+  if (plan.grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  const dim3 grid((unsigned)plan.grid + a.rest_blocks);
+  if (plan.bm == 256)
+    hipLaunchKernelGGL((grouped_fp8_kernel<256, 256, 2, 4, 2>), grid, dim3(512), 0, st, a);
+  else
+    hipLaunchKernelGGL((grouped_fp8_kernel<128, 128, 2, 2, 2>), grid, dim3(256), 0, st, a);
   return hipGetLastError();
 }
 

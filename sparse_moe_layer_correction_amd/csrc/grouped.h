@@ -32,12 +32,100 @@ struct GroupedArgs {
   int64_t b_estride, c_estride;// elements between experts (B of forward / dgrad, C of wgrad)
   int M, N;                    // wgrad: rows / columns of C; else N = columns of C
   int Kd;                      // forward, dgrad: reduction length
-  const TileRec* tiles;        // forward, dgrad: M tile table
+  const TileRec* tiles;        // forward, dgrad: M tile table; null: each wave finds its tile in the offsets
   const int32_t* n_mtiles;     //   valid entries
-  const int2* ranges;          // wgrad: rows of each expert
+  const int2* ranges;          // wgrad: rows of each expert; null as above
+  const int32_t* offsets;      // [E + 1]
+  int E, R;
+  int rest_blocks;             // without a table: the grid's last workgroups zero the rows of no expert
   int mtiles, ntiles;          // wgrad: tiles of one expert's C; else ntiles = column tiles
   int accumulate;              // wgrad: add to what C holds
 };
+
+// Finds, in one wave and from the offsets alone, what the tile table holds: lane
+// l takes the C = ceil(E / 64) experts from l * C on. About 1.5 us for a
+// workgroup, against a launch of its own for the table: taken for the grids of
+// few workgroups (grouped.hip).
+struct OffsetScan {
+  const int32_t* off;
+  int E, R, C, e0;
+  int base;            // the running maximum before the lane's experts
+  __device__ __forceinline__ int at(int i) const { return min(max(off[min(i, E)], 0), R); }
+  __device__ __forceinline__ OffsetScan(const int32_t* offsets, int E_, int R_, int lane) : off(offsets), E(E_), R(R_) {
+    C = (E + kWave - 1) / kWave;
+    e0 = lane * C;
+    int v = 0;
+    for (int j = 0; j < C; ++j) v = max(v, at(e0 + j));
+#pragma unroll
+    for (int d = 1; d < kWave; d <<= 1) {
+      const int o = __shfl_up(v, d, kWave);
+      if (lane >= d) v = max(v, o);
+    }
+    const int before = __shfl_up(v, 1, kWave);
+    base = lane == 0 ? 0 : before;
+  }
+  // f(e, lo, hi) for the lane's experts in order
+  template <typename F>
+  __device__ __forceinline__ void each(F&& f) const {
+    int v = base;
+    for (int j = 0; j < C && e0 + j < E; ++j) {
+      const int lo = max(v, at(e0 + j)), hi = max(lo, at(e0 + j + 1));
+      f(e0 + j, lo, hi);
+      v = lo;
+    }
+  }
+  // rows of expert e, the same in every lane
+  __device__ __forceinline__ int2 rows(int e) const {
+    int lo = 0, hi = 0;
+    each([&](int i, int a, int b) {
+      if (i == e) { lo = a; hi = b; }
+    });
+    const int src = e / C;
+    return make_int2(__builtin_amdgcn_readlane(lo, src), __builtin_amdgcn_readlane(hi, src));
+  }
+  // M tiles of BM rows over all experts (incl: up to and with the lane's), and
+  // the record of the expert that holds M tile mtile of them
+  __device__ __forceinline__ int tiles(int BM, int& incl) const {
+    int n = 0;
+    each([&](int, int a, int b) { n += (b - a + BM - 1) / BM; });
+    incl = wave_inclusive_scan_i32(n);
+    return __builtin_amdgcn_readlane(incl, kWave - 1);
+  }
+  __device__ __forceinline__ TileRec find(int BM, int mtile, int incl) const {
+    int first = incl, e = 0, f = 0, lo = 0, hi = 0;
+    each([&](int, int a, int b) { first -= (b - a + BM - 1) / BM; });
+    const bool mine = first <= mtile && mtile < incl;
+    each([&](int i, int a, int b) {
+      const int n = (b - a + BM - 1) / BM;
+      if (first <= mtile && mtile < first + n) { e = i; f = first; lo = a; hi = b; }
+      first += n;
+    });
+    const int src = __builtin_ctzll(__ballot(mine));
+    return make_int4(__builtin_amdgcn_readlane(e, src), __builtin_amdgcn_readlane(f, src),
+                     __builtin_amdgcn_readlane(lo, src), __builtin_amdgcn_readlane(hi, src));
+  }
+  // the rows of no expert: [0, begin) and [end, R)
+  __device__ __forceinline__ int2 covered() const {
+    int lo = R, hi = 0;
+    each([&](int i, int a, int b) {
+      if (i == 0) lo = a;
+      hi = b;
+    });
+    const int last = (E - 1) / C;
+    return make_int2(__builtin_amdgcn_readlane(lo, 0), __builtin_amdgcn_readlane(hi, last));
+  }
+};
+
+// zeroes the rows of no expert, by workgroup i of n with nt threads
+__device__ __forceinline__ void zero_rest(uint16_t* C, int64_t ldc, int N, int begin, int end, int R, int i, int n,
+                                          int nt) {
+  const int cpr = N / 8;
+  const int64_t total = (int64_t)(begin + R - end) * cpr;
+  for (int64_t j = (int64_t)i * nt + threadIdx.x; j < total; j += (int64_t)n * nt) {
+    const int64_t q = j / cpr, r = q < begin ? q : end + (q - begin);
+    *reinterpret_cast<u32x4*>(C + r * ldc + (j - q * cpr) * 8) = u32x4{0u, 0u, 0u, 0u};
+  }
+}
 
 enum GroupedForm : int { FORM_NT = 0, FORM_NN = 1, FORM_TN = 2 };   // forward, dgrad, wgrad
 
@@ -246,17 +334,37 @@ grouped_kernel(const GroupedArgs P) {
     m0 = __builtin_amdgcn_readfirstlane(mt * BM);
     n0 = __builtin_amdgcn_readfirstlane(nt * BN);
     mend = P.M;
-    const int lo = __builtin_amdgcn_readfirstlane(P.ranges[e].x);
-    Kd = __builtin_amdgcn_readfirstlane(P.ranges[e].y) - lo;
+    int2 rg;
+    if (P.ranges != nullptr) rg = P.ranges[e];
+    else rg = OffsetScan(P.offsets, P.E, P.R, lane).rows(e);
+    const int lo = __builtin_amdgcn_readfirstlane(rg.x);
+    Kd = __builtin_amdgcn_readfirstlane(rg.y) - lo;
     if (Kd <= 0 && P.accumulate) return;
     Ap = P.A + (int64_t)lo * P.lda + m0;
     Bp = P.B + (int64_t)lo * P.ldb + n0;
     c_base = (int64_t)e * P.c_estride;
   } else {
-    const int valid = *P.n_mtiles * P.ntiles;
-    if ((int)blockIdx.x >= valid) return;
-    const int t = xcd_remap(blockIdx.x, valid);
-    const TileRec rec = P.tiles[t / P.ntiles];
+    int valid, t;
+    TileRec rec;
+    if (P.tiles != nullptr) {
+      valid = *P.n_mtiles * P.ntiles;
+      if ((int)blockIdx.x >= valid) return;
+      t = xcd_remap(blockIdx.x, valid);
+      rec = P.tiles[t / P.ntiles];
+    } else {
+      const OffsetScan scan(P.offsets, P.E, P.R, lane);
+      const int grid = (int)gridDim.x - P.rest_blocks;
+      if ((int)blockIdx.x >= grid) {
+        const int2 c = scan.covered();
+        zero_rest(static_cast<uint16_t*>(P.C), P.ldc, P.N, c.x, c.y, P.R, (int)blockIdx.x - grid, P.rest_blocks, NT);
+        return;
+      }
+      int incl;
+      valid = scan.tiles(BM, incl) * P.ntiles;
+      if ((int)blockIdx.x >= valid) return;
+      t = xcd_remap(blockIdx.x, valid);
+      rec = scan.find(BM, t / P.ntiles, incl);
+    }
     const int e = __builtin_amdgcn_readfirstlane(rec.x), first = __builtin_amdgcn_readfirstlane(rec.y);
     const int lo = __builtin_amdgcn_readfirstlane(rec.z), hi = __builtin_amdgcn_readfirstlane(rec.w);
     int mt, nt;

@@ -30,17 +30,10 @@ __global__ void __launch_bounds__(1024) grouped_tiles_kernel(const int32_t* __re
   __syncthreads();
   for (int w = 0; w < wave; ++w) v = max(v, wmax[w]);
   if (blockIdx.x > 0) {
-    int end = 0;                                             // the highest offset
-    __shared__ int top;
-    if (tid == E - 1) top = max(v, clamped(E));
+    __shared__ int end;                                      // the highest offset
+    if (tid == E - 1) end = max(v, clamped(E));
     __syncthreads();
-    end = top;
-    const int cpr = rest.N / 8, begin = clamped(0);
-    const int64_t n = (int64_t)(begin + R - end) * cpr;
-    for (int64_t i = (int64_t)(blockIdx.x - 1) * 1024 + tid; i < n; i += (int64_t)kRestBlocks * 1024) {
-      const int64_t q = i / cpr, r = q < begin ? q : end + (q - begin);
-      *reinterpret_cast<u32x4*>(rest.C + r * rest.ldc + (i - q * cpr) * 8) = u32x4{0u, 0u, 0u, 0u};
-    }
+    zero_rest(rest.C, rest.ldc, rest.N, clamped(0), end, R, (int)blockIdx.x - 1, kRestBlocks, 1024);
     return;
   }
   const int lo = v;
@@ -84,9 +77,37 @@ static void launch_form(const GroupedArgs& a, int BM, int64_t grid, hipStream_t 
     hipLaunchKernelGGL((grouped_kernel<FORM, 128, 128, 2, 2, 2, OUT, 2>), dim3((unsigned)grid), dim3(256), 0, st, a);
 }
 
+// Which tiles, from what the host knows (the rows' number, not how they spread).
+// 256-row tiles where an expert has 128 rows or more on average; else 128.
 int grouped_bm(int64_t R, int E) { return R >= (int64_t)E * 128 ? 256 : 128; }
 
-hipError_t launch_grouped_rows(const GroupedProduct& p, const GroupedScratch& s, int BM, hipStream_t st) {
+// Grids of at most this many workgroups find their tiles in the offsets
+// (OffsetScan) and need no table.
+constexpr int64_t kScanGrid = 1024;
+constexpr int kScanExperts = 128;
+
+GroupedPlan grouped_rows_plan(int64_t R, int E, int N) {
+  GroupedPlan p;
+  p.bm = grouped_bm(R, E);
+  p.mtiles = 0;
+  p.ntiles = (N + p.bm - 1) / p.bm;
+  p.grid = grouped_max_tiles(R, E, p.bm) * p.ntiles;
+  p.scan = p.grid <= kScanGrid && E <= kScanExperts;
+  return p;
+}
+
+GroupedPlan grouped_wgrad_plan(int E, int M, int N) {
+  GroupedPlan p;
+  p.bm = (int64_t)E * ((M + 255) / 256) * ((N + 255) / 256) >= 256 ? 256 : 128;
+  p.mtiles = (M + p.bm - 1) / p.bm;
+  p.ntiles = (N + p.bm - 1) / p.bm;
+  p.grid = (int64_t)E * p.mtiles * p.ntiles;
+  p.scan = p.grid <= kScanGrid && E <= kScanExperts;
+  return p;
+}
+
+hipError_t launch_grouped_rows(const GroupedProduct& p, const GroupedPlan& plan, const GroupedScratch& s, bool rest,
+                               hipStream_t st) {
   GroupedArgs a{};
   a.A = p.A;
   a.B = p.B;
@@ -97,18 +118,22 @@ hipError_t launch_grouped_rows(const GroupedProduct& p, const GroupedScratch& s,
   a.b_estride = p.estride;
   a.N = p.N;
   a.Kd = p.Kd;
-  a.tiles = s.tiles;
+  a.tiles = plan.scan ? nullptr : s.tiles;
   a.n_mtiles = s.n_mtiles;
-  a.ntiles = (p.N + BM - 1) / BM;
-  const int64_t grid = grouped_max_tiles(p.R, p.E, BM) * a.ntiles;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-  if (p.transposed_b) launch_form<FORM_NN, EPI_BF16>(a, BM, grid, st);
-  else launch_form<FORM_NT, EPI_BF16>(a, BM, grid, st);
+  a.offsets = p.offsets;
+  a.E = p.E;
+  a.R = (int)p.R;
+  a.rest_blocks = plan.scan && rest ? kScanRestBlocks : 0;
+  a.ntiles = plan.ntiles;
+  if (plan.grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  const int64_t grid = plan.grid + a.rest_blocks;
+  if (p.transposed_b) launch_form<FORM_NN, EPI_BF16>(a, plan.bm, grid, st);
+  else launch_form<FORM_NT, EPI_BF16>(a, plan.bm, grid, st);
   return hipGetLastError();
 }
 
-hipError_t launch_grouped_wgrad(const GroupedProduct& p, int M, bool f32, bool accumulate, const GroupedScratch& s,
-                                hipStream_t st) {
+hipError_t launch_grouped_wgrad(const GroupedProduct& p, int M, bool f32, bool accumulate, const GroupedPlan& plan,
+                                const GroupedScratch& s, hipStream_t st) {
   GroupedArgs a{};
   a.A = p.A;
   a.B = p.B;
@@ -119,18 +144,16 @@ hipError_t launch_grouped_wgrad(const GroupedProduct& p, int M, bool f32, bool a
   a.c_estride = p.estride;
   a.M = M;
   a.N = p.N;
-  a.ranges = s.ranges;
-#ifndef WG_BM
-#define WG_BM ((int64_t)p.E * ((M + 255) / 256) * ((p.N + 255) / 256) >= 256 ? 256 : 128)
-#endif
-  const int BM = WG_BM;
-  a.mtiles = (M + BM - 1) / BM;
-  a.ntiles = (p.N + BM - 1) / BM;
+  a.ranges = plan.scan ? nullptr : s.ranges;
+  a.offsets = p.offsets;
+  a.E = p.E;
+  a.R = (int)p.R;
+  a.mtiles = plan.mtiles;
+  a.ntiles = plan.ntiles;
   a.accumulate = accumulate;
-  const int64_t grid = (int64_t)p.E * a.mtiles * a.ntiles;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-  if (f32) launch_form<FORM_TN, EPI_F32>(a, BM, grid, st);
-  else launch_form<FORM_TN, EPI_BF16>(a, BM, grid, st);
+  if (plan.grid > 0x7FFFFFFF) return hipErrorInvalidValue;
+  if (f32) launch_form<FORM_TN, EPI_F32>(a, plan.bm, plan.grid, st);
+  else launch_form<FORM_TN, EPI_BF16>(a, plan.bm, plan.grid, st);
   return hipGetLastError();
 }
 

@@ -24,7 +24,18 @@ struct GroupedProduct {
   int64_t R;
   int E, N, Kd;
   bool transposed_b;   // B stored [Kd, N]
+  const int32_t* offsets;
 };
+
+// Tiles and grid of one product.
+struct GroupedPlan {
+  int bm, mtiles, ntiles;
+  int64_t grid;
+  bool scan;           // the kernel finds its tiles itself; else it needs launch_grouped_tiles
+};
+constexpr int kScanRestBlocks = 16;   // workgroups that zero the rows of no expert, without a table
+GroupedPlan grouped_rows_plan(int64_t R, int E, int N);
+GroupedPlan grouped_wgrad_plan(int E, int M, int N);
 
 // Output whose rows of no expert are to be zeroed (C null: none).
 struct RestRows {
@@ -33,12 +44,13 @@ struct RestRows {
   int N;               // multiple of 8
 };
 
-int grouped_bm(int64_t R, int E);
 hipError_t launch_grouped_tiles(const int32_t* offsets, int E, int R, int BM, const GroupedScratch& s,
                                 const RestRows& rest, hipStream_t st);
-hipError_t launch_grouped_rows(const GroupedProduct& p, const GroupedScratch& s, int BM, hipStream_t st);
-hipError_t launch_grouped_wgrad(const GroupedProduct& p, int M, bool f32, bool accumulate, const GroupedScratch& s,
-                                hipStream_t st);
+// rest: without a table, also zero C's rows of no expert
+hipError_t launch_grouped_rows(const GroupedProduct& p, const GroupedPlan& plan, const GroupedScratch& s, bool rest,
+                               hipStream_t st);
+hipError_t launch_grouped_wgrad(const GroupedProduct& p, int M, bool f32, bool accumulate, const GroupedPlan& plan,
+                                const GroupedScratch& s, hipStream_t st);
 
 // E4M3 codes, one scale per 128 (fp8.h)
 struct Fp8Args {
@@ -49,15 +61,18 @@ struct Fp8Args {
   uint16_t* C;
   int64_t ldc, R;
   int N, K, nb, kb;
-  const int4* tiles;
+  const int4* tiles;           // null: found in the offsets
   const int32_t* n_mtiles;
+  const int32_t* offsets;
+  int E, rest_blocks;
   int ntiles;
 };
+GroupedPlan fp8_plan(int64_t R, int E, int N);
 hipError_t launch_fp8_rows(const uint16_t* x, int64_t R, int K, int64_t ldx, uint8_t* codes, float* scales,
                            hipStream_t st);
 hipError_t launch_fp8_blocks(const uint16_t* w, int64_t count, int N, int K, uint8_t* codes, float* scales,
                              hipStream_t st);
-hipError_t launch_grouped_fp8(const Fp8Args& a, int64_t R, int E, int BM, hipStream_t st);
+hipError_t launch_grouped_fp8(const Fp8Args& a, const GroupedPlan& plan, hipStream_t st);
 
 // Gradient tensors of one launch; entry i's chunks of kGradChunk elements are
 // first[i] .. first[i + 1] of the launch's (the last entry's end at chunks).

@@ -93,11 +93,12 @@ int moe_grouped_matmul(const moe_grouped_dims* dims, const uint16_t* x, const ui
   if (!ws_ok(ws, ws_bytes, l.total)) return MOE_ERR_WORKSPACE;
   if (d.R == 0) return MOE_OK;
   const GroupedScratch s = grouped_scratch(l, ws);
-  const int BM = grouped_bm(d.R, d.E);
+  const GroupedPlan plan = grouped_rows_plan(d.R, d.E, d.N);
   const RestRows rest{d.zero_rest ? y : nullptr, d.ldy, d.N};
-  if (launch_grouped_tiles(offsets, d.E, (int)d.R, BM, s, rest, stream) != hipSuccess) return MOE_ERR_HIP;
-  const GroupedProduct p{x, w, y, d.ldx, d.ldw, d.ldy, d.w_stride, d.R, d.E, d.N, d.K, false};
-  return hip_status(launch_grouped_rows(p, s, BM, stream));
+  if (!plan.scan && launch_grouped_tiles(offsets, d.E, (int)d.R, plan.bm, s, rest, stream) != hipSuccess)
+    return MOE_ERR_HIP;
+  const GroupedProduct p{x, w, y, d.ldx, d.ldw, d.ldy, d.w_stride, d.R, d.E, d.N, d.K, false, offsets};
+  return hip_status(launch_grouped_rows(p, plan, s, d.zero_rest != 0, stream));
 }
 
 int moe_grouped_matmul_grad(const moe_grouped_dims* dims, const uint16_t* dy, const uint16_t* x, const uint16_t* w,
@@ -113,16 +114,18 @@ int moe_grouped_matmul_grad(const moe_grouped_dims* dims, const uint16_t* dy, co
   const GroupedLayout l = grouped_layout(d);
   if (!ws_ok(ws, ws_bytes, l.total)) return MOE_ERR_WORKSPACE;
   const GroupedScratch s = grouped_scratch(l, ws);
-  const int BM = grouped_bm(d.R, d.E);
-  const RestRows rest{d.zero_rest ? dx : nullptr, d.lddx, d.K};
-  if (launch_grouped_tiles(offsets, d.E, (int)d.R, BM, s, rest, stream) != hipSuccess) return MOE_ERR_HIP;
-  if (dx && d.R > 0) {
-    const GroupedProduct p{dy, w, dx, d.ldy, d.ldw, d.lddx, d.w_stride, d.R, d.E, d.K, d.N, true};
-    if (launch_grouped_rows(p, s, BM, stream) != hipSuccess) return MOE_ERR_HIP;
+  const GroupedPlan rows = grouped_rows_plan(d.R, d.E, d.K), wg = grouped_wgrad_plan(d.E, d.N, d.K);
+  const bool run_dx = dx && d.R > 0;
+  const RestRows rest{run_dx && !rows.scan && d.zero_rest ? dx : nullptr, d.lddx, d.K};
+  if ((run_dx && !rows.scan) || (dw && !wg.scan))
+    if (launch_grouped_tiles(offsets, d.E, (int)d.R, rows.bm, s, rest, stream) != hipSuccess) return MOE_ERR_HIP;
+  if (run_dx) {
+    const GroupedProduct p{dy, w, dx, d.ldy, d.ldw, d.lddx, d.w_stride, d.R, d.E, d.K, d.N, true, offsets};
+    if (launch_grouped_rows(p, rows, s, d.zero_rest != 0, stream) != hipSuccess) return MOE_ERR_HIP;
   }
   if (dw) {
-    const GroupedProduct p{dy, x, dw, d.ldy, d.ldx, d.K, (int64_t)d.N * d.K, d.R, d.E, d.K, 0, true};
-    if (launch_grouped_wgrad(p, d.N, dw_dtype == MOE_FP32, accumulate != 0, s, stream) != hipSuccess)
+    const GroupedProduct p{dy, x, dw, d.ldy, d.ldx, d.K, (int64_t)d.N * d.K, d.R, d.E, d.K, 0, true, offsets};
+    if (launch_grouped_wgrad(p, d.N, dw_dtype == MOE_FP32, accumulate != 0, wg, s, stream) != hipSuccess)
       return MOE_ERR_HIP;
   }
   return MOE_OK;
@@ -161,9 +164,10 @@ int moe_grouped_matmul_fp8(const moe_grouped_dims* dims, const uint8_t* xq, cons
   if (!ws_ok(ws, ws_bytes, l.total)) return MOE_ERR_WORKSPACE;
   if (d.R == 0) return MOE_OK;
   const GroupedScratch s = grouped_scratch(l, ws);
-  const int BM = 128;
-  const RestRows rest{d.zero_rest ? y : nullptr, d.ldy, d.N};
-  if (launch_grouped_tiles(offsets, d.E, (int)d.R, BM, s, rest, stream) != hipSuccess) return MOE_ERR_HIP;
+  const GroupedPlan plan = fp8_plan(d.R, d.E, d.N);
+  const RestRows rest{!plan.scan && d.zero_rest ? y : nullptr, d.ldy, d.N};
+  if (!plan.scan && launch_grouped_tiles(offsets, d.E, (int)d.R, plan.bm, s, rest, stream) != hipSuccess)
+    return MOE_ERR_HIP;
   Fp8Args a{};
   a.A = xq;
   a.sx = xs;
@@ -176,10 +180,13 @@ int moe_grouped_matmul_fp8(const moe_grouped_dims* dims, const uint8_t* xq, cons
   a.K = d.K;
   a.nb = (d.N + 127) / 128;
   a.kb = (d.K + 127) / 128;
-  a.tiles = s.tiles;
+  a.tiles = plan.scan ? nullptr : s.tiles;
   a.n_mtiles = s.n_mtiles;
-  a.ntiles = (d.N + 127) / 128;
-  return hip_status(launch_grouped_fp8(a, d.R, d.E, BM, stream));
+  a.offsets = offsets;
+  a.E = d.E;
+  a.rest_blocks = plan.scan && d.zero_rest ? kScanRestBlocks : 0;
+  a.ntiles = plan.ntiles;
+  return hip_status(launch_grouped_fp8(a, plan, stream));
 }
 
 }  // extern "C"
