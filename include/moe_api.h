@@ -89,7 +89,7 @@ enum moe_status {
   MOE_OK = 0,
   MOE_ERR_INVALID = -1,      /* null pointer, non-positive size, K > E, bad C, bad groups */
   MOE_ERR_UNSUPPORTED = -2,  /* H, L, I or Is not a multiple of 64; E > 1024; K > 64;
-                                T*K >= 2^31; 2*T*L >= 2^32 */
+                                T*K >= 2^31; 2*T*L >= 2^32; as the grouped calls state */
   MOE_ERR_WORKSPACE = -3,    /* workspace null, too small or not 256-byte aligned */
   MOE_ERR_HIP = -4,          /* a HIP launch failed */
   MOE_ERR_TOO_LARGE = -5     /* moe_forward_noalloc: the forward needs more than its static scratch */
@@ -328,7 +328,8 @@ int moe_forward_noalloc(const moe_dims* dims, const moe_weights* w, const uint16
  * below the weight's extent), null or not 16-byte aligned tensors.
  * MOE_ERR_UNSUPPORTED: N, K or a stride not a multiple of 8 (the kernels move 16
  * bytes per lane; K a multiple of 16 for the 8-bit product), E > 1024,
- * R >= 2^31, a row stride >= 2^22, a product of 2^31 tiles or more.
+ * R >= 2^31, a row stride >= 2^22, a product of 2^23 tiles (of 128 x 128 or
+ * more) or more.
  * Outputs may not overlap inputs. R = 0 is valid (its row tensors may be null). */
 typedef struct moe_grouped_dims {
   int64_t R;
@@ -337,10 +338,12 @@ typedef struct moe_grouped_dims {
   int32_t zero_rest;
 } moe_grouped_dims;
 
-/* Bytes of the workspace (256-byte aligned, device) of the calls below that
- * take a moe_grouped_dims; 0 for dims they refuse. Nothing in it has to be
- * zero, and nothing in it is used by a later call: calls that overlap in time
- * need a workspace each. */
+/* Bytes of a workspace (256-byte aligned, device) that is enough for each of the
+ * calls below that take a moe_grouped_dims; 0 for dims they refuse. A call that
+ * needs less takes less: MOE_ERR_WORKSPACE, before any launch, says that it
+ * needs more than it was given, and a call on few rows and experts may take a
+ * NULL one. Nothing in it has to be zero, and nothing in it is used by a later
+ * call: calls that overlap in time need a workspace each. */
 size_t moe_grouped_workspace_bytes(const moe_grouped_dims* dims);
 
 /* y[r, n] = sum_k x[r, k] W[e(r)][n, k]: x, w, y device bf16, fp32 sums, one
@@ -372,8 +375,8 @@ int moe_grouped_matmul_grad(const moe_grouped_dims* dims, const uint16_t* dy, co
  *   blocks: w [count, N, K] bf16 dense, blocks of 128 x 128:
  *           codes [count, N, K], scales [count, ceil(N/128), ceil(K/128)]
  * MOE_ERR_INVALID: R, count < 0, N, K <= 0, ldx < K, null or not 16-byte aligned
- * x, w, codes; MOE_ERR_UNSUPPORTED: K or ldx not a multiple of 8, 2^31 blocks or
- * more, N * K >= 2^31. */
+ * x, w, codes; MOE_ERR_UNSUPPORTED: K or ldx not a multiple of 8, 2^28 blocks of
+ * rows or 2^24 blocks of weights or more, N * K >= 2^31. */
 int moe_quantize_fp8_rows(const uint16_t* x, int64_t R, int32_t K, int64_t ldx, uint8_t* codes, float* scales,
                           hipStream_t stream);
 int moe_quantize_fp8_blocks(const uint16_t* w, int64_t count, int32_t N, int32_t K, uint8_t* codes, float* scales,
@@ -387,6 +390,12 @@ int moe_quantize_fp8_blocks(const uint16_t* w, int64_t count, int32_t N, int32_t
 int moe_grouped_matmul_fp8(const moe_grouped_dims* dims, const uint8_t* xq, const float* xs, const uint8_t* wq,
                            const float* w_scale, const int32_t* offsets, uint16_t* y, void* ws, size_t ws_bytes,
                            hipStream_t stream);
+
+/* The same from bf16 rows x [R, K] (row stride ldx): moe_quantize_fp8_rows into
+ * the workspace, then the product; the same bits. */
+int moe_grouped_matmul_fp8_rows(const moe_grouped_dims* dims, const uint16_t* x, const uint8_t* wq,
+                                const float* w_scale, const int32_t* offsets, uint16_t* y, void* ws, size_t ws_bytes,
+                                hipStream_t stream);
 
 /* ---- the end of a training step: global gradient norm and clipping ---- */
 

@@ -39,7 +39,8 @@ EXPORTS = (
     "moe_abi_version", "moe_quantize_mxfp8", "moe_forward_mx", "moe_forward_mx_profiled",
     "moe_rmsnorm", "moe_block_workspace_bytes", "moe_block_forward", "moe_bias_update", "moe_quantize_mxfp4",
     "moe_forward_noalloc", "moe_grouped_workspace_bytes", "moe_grouped_matmul", "moe_grouped_matmul_grad",
-    "moe_quantize_fp8_rows", "moe_quantize_fp8_blocks", "moe_grouped_matmul_fp8", "moe_grad_norm_workspace_bytes",
+    "moe_quantize_fp8_rows", "moe_quantize_fp8_blocks", "moe_grouped_matmul_fp8", "moe_grouped_matmul_fp8_rows",
+    "moe_grad_norm_workspace_bytes",
     "moe_grad_norm", "moe_clip_grad_norm",
 )
 
@@ -158,6 +159,7 @@ def load_library(path: Optional[str] = None):
         "moe_quantize_fp8_rows": (i32, [vp, ctypes.c_int64, ctypes.c_int32, ctypes.c_int64, vp, vp, vp]),
         "moe_quantize_fp8_blocks": (i32, [vp, ctypes.c_int64, ctypes.c_int32, ctypes.c_int32, vp, vp, vp]),
         "moe_grouped_matmul_fp8": (i32, [ctypes.POINTER(_GroupedDims), vp, vp, vp, vp, vp, vp, vp, sz, vp]),
+        "moe_grouped_matmul_fp8_rows": (i32, [ctypes.POINTER(_GroupedDims), vp, vp, vp, vp, vp, vp, sz, vp]),
         "moe_grad_norm_workspace_bytes": (sz, [ctypes.POINTER(_GradTensor), ctypes.c_int32]),
         "moe_grad_norm": (i32, [ctypes.POINTER(_GradTensor), ctypes.c_int32, vp, vp, sz, vp]),
         "moe_clip_grad_norm": (i32, [ctypes.POINTER(_GradTensor), ctypes.c_int32, ctypes.c_float, vp, vp, sz, vp]),
@@ -616,15 +618,27 @@ def _need_matrix(t, name):
         raise ValueError(f"{name} must have 2 dimensions, got shape {tuple(t.shape)}")
 
 
-def _grouped_ws(lib, d: _GroupedDims, device, ws):
-    """The workspace's address and size (and the tensor, which the caller keeps until the launch)."""
+_ERR_WORKSPACE = -3
+
+
+def _grouped_call(fn, d: _GroupedDims, device, ws, *args):
+    """fn(d, *args, ws, ws_bytes, stream) on the current stream. Without a caller's workspace
+    the first try has none, which small calls do not need; the others refuse before any
+    launch and get one."""
+    dr = ctypes.byref(d)
+    stream = _raw_stream(device)
     if ws is None:
-        nbytes = lib.moe_grouped_workspace_bytes(ctypes.byref(d))
-        ws = _torch().empty(max(nbytes, 1), dtype=_torch().uint8, device=device)
-        return ws, nbytes
-    if ws.device != device:
-        raise ValueError(f"ws must be on the GPU device {device}")
-    return ws, ws.numel() * ws.element_size()
+        rc = fn(dr, *args, None, 0, stream)
+        if rc == _ERR_WORKSPACE:
+            nbytes = load_library().moe_grouped_workspace_bytes(dr)
+            ws = _torch().empty(nbytes, dtype=_torch().uint8, device=device)
+            rc = fn(dr, *args, ws.data_ptr(), nbytes, stream)
+    else:
+        if ws.device != device:
+            raise ValueError(f"ws must be on the GPU device {device}")
+        rc = fn(dr, *args, ws.data_ptr(), ws.numel() * ws.element_size(), stream)
+    if rc != 0:
+        _check(rc)
 
 
 def grouped_workspace_bytes(R: int, E: int, N: int, K: int) -> int:
@@ -656,9 +670,7 @@ def grouped_matmul(x, w, offsets, *, out=None, ws=None, stream=None):
         ldy = _need_rows(out, "out", torch.bfloat16, R, N, dev)
     lib = load_library()
     d = _GroupedDims(R, E, N, K, ldx, ldy, ldw, es, 0, fresh)
-    ws, nbytes = _grouped_ws(lib, d, dev, ws)
-    _check(lib.moe_grouped_matmul(ctypes.byref(d), x.data_ptr(), w.data_ptr(), offsets.data_ptr(), out.data_ptr(),
-                                  ws.data_ptr(), nbytes, _raw_stream(dev)))
+    _grouped_call(lib.moe_grouped_matmul, d, dev, ws, x.data_ptr(), w.data_ptr(), offsets.data_ptr(), out.data_ptr())
     return out
 
 
@@ -705,10 +717,8 @@ def grouped_matmul_grad(dy, x, w, offsets, *, need_dx: bool = True, need_dw: boo
         _need(dw, "dw", dw_dtype, (E, N, K), dev)
     lib = load_library()
     d = _GroupedDims(R, E, N, K, ldx, ldy, ldw, es, lddx, fresh)
-    ws, nbytes = _grouped_ws(lib, d, dev, ws)
-    _check(lib.moe_grouped_matmul_grad(ctypes.byref(d), dy.data_ptr(), x.data_ptr(), w.data_ptr(), offsets.data_ptr(),
-                                       _ptr(dx), _ptr(dw), dw_dtype == torch.float32, accumulate, ws.data_ptr(),
-                                       nbytes, _raw_stream(dev)))
+    _grouped_call(lib.moe_grouped_matmul_grad, d, dev, ws, dy.data_ptr(), x.data_ptr(), w.data_ptr(),
+                  offsets.data_ptr(), _ptr(dx), _ptr(dw), dw_dtype == torch.float32, accumulate)
     return dx, dw
 
 
@@ -771,8 +781,9 @@ def grouped_matmul_fp8(x, w_codes, w_scale, offsets, *, x_scale=None, out=None, 
     if not w_codes.is_contiguous():
         raise ValueError("w_codes must be contiguous")
     _need(w_scale, "w_scale", torch.float32, (E, nb, kb), dev)
+    ldx = 0
     if x_scale is None:
-        _need_rows(x, "x", torch.bfloat16, R, K, dev)
+        ldx = _need_rows(x, "x", torch.bfloat16, R, K, dev)
     else:
         _need(x, "x", torch.uint8, (R, K), dev)
         _need(x_scale, "x_scale", torch.float32, (kb, R), dev)
@@ -782,14 +793,14 @@ def grouped_matmul_fp8(x, w_codes, w_scale, offsets, *, x_scale=None, out=None, 
         ldy = N
     else:
         ldy = _need_rows(out, "out", torch.bfloat16, R, N, dev)
-    if x_scale is None:
-        x, x_scale = quantize_fp8_rows(x)
     lib = load_library()
-    d = _GroupedDims(R, E, N, K, 0, ldy, 0, 0, 0, fresh)
-    ws, nbytes = _grouped_ws(lib, d, dev, ws)
-    _check(lib.moe_grouped_matmul_fp8(ctypes.byref(d), x.data_ptr(), x_scale.data_ptr(), w_codes.data_ptr(),
-                                      w_scale.data_ptr(), offsets.data_ptr(), out.data_ptr(), ws.data_ptr(), nbytes,
-                                      _raw_stream(dev)))
+    d = _GroupedDims(R, E, N, K, ldx, ldy, 0, 0, 0, fresh)
+    if x_scale is None:
+        _grouped_call(lib.moe_grouped_matmul_fp8_rows, d, dev, ws, x.data_ptr(), w_codes.data_ptr(),
+                      w_scale.data_ptr(), offsets.data_ptr(), out.data_ptr())
+    else:
+        _grouped_call(lib.moe_grouped_matmul_fp8, d, dev, ws, x.data_ptr(), x_scale.data_ptr(), w_codes.data_ptr(),
+                      w_scale.data_ptr(), offsets.data_ptr(), out.data_ptr())
     return out
 
 

@@ -93,7 +93,6 @@ hipError_t launch_fp8_rows(const uint16_t* x, int64_t R, int K, int64_t ldx, uin
   const int kb = (K + 127) / 128;
   const int64_t grid = (R * kb + 15) / 16;
   if (grid == 0) return hipSuccess;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
   hipLaunchKernelGGL(fp8_rows_kernel, dim3((unsigned)grid), dim3(256), 0, st, x, R, K, ldx, kb, codes, scales);
   return hipGetLastError();
 }
@@ -138,23 +137,11 @@ hipError_t launch_fp8_blocks(const uint16_t* w, int64_t count, int N, int K, uin
   const int nb = (N + 127) / 128, kb = (K + 127) / 128;
   const int64_t grid = count * nb * kb;
   if (grid == 0) return hipSuccess;
-  if (grid > 0x7FFFFFFF) return hipErrorInvalidValue;
   hipLaunchKernelGGL(fp8_blocks_kernel, dim3((unsigned)grid), dim3(256), 0, st, w, N, K, nb, kb, codes, scales);
   return hipGetLastError();
 }
 
-GroupedPlan fp8_plan(int64_t R, int E, int N) {
-  GroupedPlan p;
-  p.bm = R >= (int64_t)E * 128 ? 256 : 128;
-  p.mtiles = 0;
-  p.ntiles = (N + p.bm - 1) / p.bm;
-  p.grid = grouped_max_tiles(R, E, p.bm) * p.ntiles;
-  p.scan = p.grid <= 1024 && E <= 128;
-  return p;
-}
-
 hipError_t launch_grouped_fp8(const Fp8Args& a, const GroupedPlan& plan, hipStream_t st) {
-  if (plan.grid > 0x7FFFFFFF) return hipErrorInvalidValue;
   const dim3 grid((unsigned)plan.grid + a.rest_blocks);
   if (plan.bm == 256)
     hipLaunchKernelGGL((grouped_fp8_kernel<256, 256, 2, 4, 2>), grid, dim3(512), 0, st, a);

@@ -40,6 +40,8 @@ struct GroupedArgs {
   int rest_blocks;             // without a table: the grid's last workgroups zero the rows of no expert
   int mtiles, ntiles;          // wgrad: tiles of one expert's C; else ntiles = column tiles
   int accumulate;              // wgrad: add to what C holds
+  int split;                   // wgrad: rows of a piece (0: an expert's rows are one sum); piece i's
+                               //   fp32 sums go to C + i * c_estride
 };
 
 // Finds, in one wave and from the offsets alone, what the tile table holds: lane
@@ -310,13 +312,16 @@ __device__ __forceinline__ void store_wave_tile(const f32x16 (&acc)[WTN / 32][WT
 
 // C tile BM x BN by WM x WN waves. OUT: EPI_BF16 or EPI_F32. OCC: waves per
 // SIMD the registers are sized for.
-template <int FORM, int BM, int BN, int WM, int WN, int OCC, int OUT, int BST>
+template <int FORM, int BM, int BN, int WM, int WN, int OCC, int OUT, int AST, int BST>
 __global__ void __launch_bounds__(64 * WM * WN, 1) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
 grouped_kernel(const GroupedArgs P) {
   constexpr int NT = 64 * WM * WN;
   constexpr bool AT = FORM == FORM_TN, BT = FORM != FORM_NT;
   static_assert(BM * 8 % NT == 0 && BN * 8 % NT == 0, "tile shape");
-  __shared__ u32x4 sa0[BM * 8], sb0[BN * 8], sa1[BM * 8], sb1[BN * 8], sb2[BST == 3 ? BN * 8 : 1];
+  static_assert((AST == 2 && (BST == 2 || BST == 3)) || (AST == 4 && BST == 4), "stages");
+  constexpr bool DEEP = AST == 4;
+  __shared__ u32x4 sa0[BM * 8], sb0[BN * 8], sa1[BM * 8], sb1[BN * 8], sb2[BST >= 3 ? BN * 8 : 1];
+  __shared__ u32x4 sa2[DEEP ? BM * 8 : 1], sa3[DEEP ? BM * 8 : 1], sb3[DEEP ? BN * 8 : 1];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -327,16 +332,30 @@ grouped_kernel(const GroupedArgs P) {
   int64_t c_base = 0;
   if constexpr (FORM == FORM_TN) {
     const int per = P.mtiles * P.ntiles;
-    const int t = xcd_remap(blockIdx.x, gridDim.x);
-    const int e = __builtin_amdgcn_readfirstlane(t / per);
+    int t, e;
+    int2 rg;
+    if (P.split > 0) {
+      // pieces of an expert's rows are laid out as the M tiles of a rows product are
+      const OffsetScan scan(P.offsets, P.E, P.R, lane);
+      int incl;
+      const int valid = scan.tiles(P.split, incl) * per;
+      if ((int)blockIdx.x >= valid) return;
+      t = xcd_remap(blockIdx.x, valid);
+      e = __builtin_amdgcn_readfirstlane(t / per);       // the piece: C's index
+      const TileRec rec = scan.find(P.split, e, incl);
+      rg.x = rec.z + (e - rec.y) * P.split;
+      rg.y = min(rg.x + P.split, rec.w);
+    } else {
+      t = xcd_remap(blockIdx.x, gridDim.x);
+      e = __builtin_amdgcn_readfirstlane(t / per);
+      if (P.ranges != nullptr) rg = P.ranges[e];
+      else rg = OffsetScan(P.offsets, P.E, P.R, lane).rows(e);
+    }
     int mt, nt;
     tile_order(t - e * per, P.mtiles, P.ntiles, 4, mt, nt);
     m0 = __builtin_amdgcn_readfirstlane(mt * BM);
     n0 = __builtin_amdgcn_readfirstlane(nt * BN);
     mend = P.M;
-    int2 rg;
-    if (P.ranges != nullptr) rg = P.ranges[e];
-    else rg = OffsetScan(P.offsets, P.E, P.R, lane).rows(e);
     const int lo = __builtin_amdgcn_readfirstlane(rg.x);
     Kd = __builtin_amdgcn_readfirstlane(rg.y) - lo;
     if (Kd <= 0 && P.accumulate) return;
@@ -415,26 +434,35 @@ grouped_kernel(const GroupedArgs P) {
         for (int tm = 0; tm < TM; ++tm)
           acc[tn][tm] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.b[tn], f.a[tm], acc[tn][tm], 0, 0, 0);
     };
-    // Two LDS stages of A, BST of B. The reads of a 16-deep substep run beside
+    // AST LDS stages of A, BST of B. The reads of a 16-deep substep run beside
     // the MFMAs of the one before; the one barrier of a k tile sits before its
     // last substep, whose fragments are in registers by then: past it the next
     // tile has landed and nobody reads this tile's stages. With three stages B
     // is loaded two tiles ahead (the weights, which come from HBM while the
-    // rows stay in the caches), in the second substep of the tile before.
+    // rows stay in the caches), in the second substep of the tile before. Four
+    // stages of both (128 x 128 tiles, one workgroup to a CU) are for grids that
+    // leave CUs idle: a k tile's time is then the loads' latency over the tiles in flight.
     constexpr int NM = TM * TN, NR = TM * (AT ? 2 : 1) + TN * (BT ? 2 : 1);
     constexpr int NA = OperandLoad<H, AT, NT>::NL, NB = OperandLoad<BN, BT, NT>::NL;
-    auto stA = [&](auto v) -> u32x4* { return decltype(v)::value == 0 ? sa0 : sa1; };
+    auto stA = [&](auto v) -> u32x4* {
+      if constexpr (decltype(v)::value == 0) return sa0;
+      else if constexpr (decltype(v)::value == 1) return sa1;
+      else if constexpr (decltype(v)::value == 2) return sa2;
+      else return sa3;
+    };
     auto stB = [&](auto v) -> u32x4* {
       if constexpr (decltype(v)::value == 0) return sb0;
       else if constexpr (decltype(v)::value == 1) return sb1;
-      else return sb2;
+      else if constexpr (decltype(v)::value == 2) return sb2;
+      else return sb3;
     };
-    // s_waitcnt vmcnt(BST == 3 ? NB : 0) lgkmcnt(0): with three stages the loads of B tile kt + 2 stay in flight
-    constexpr int VM = BST == 3 ? NB : 0;
+    // s_waitcnt vmcnt(VM) lgkmcnt(0): the loads that stay in flight over a barrier are,
+    // with three stages of B, those of its tile kt + 2, with four those of the tiles kt + 2 and kt + 3
+    constexpr int VM = DEEP ? 2 * (NA + NB) : BST == 3 ? NB : 0;
     constexpr int kWait = (VM & 0xF) | (0x7 << 4) | (0x0 << 8) | (((VM >> 4) & 3) << 14);
     auto step = [&](int kt, auto sa, auto sb, auto first) {
       constexpr int SA = decltype(sa)::value, SB = decltype(sb)::value;
-      constexpr bool MID = BST == 3 && decltype(first)::value == 0;   // tile 2 was loaded before step 0
+      constexpr bool MID = BST == 3 &&  decltype(first)::value == 0;   // tile 2 was loaded before step 0
       read(f1, stA(sa), stB(sb), 1);
       mma(f0);
       interleave<NM, NR, 0>();
@@ -448,11 +476,11 @@ grouped_kernel(const GroupedArgs P) {
       __builtin_amdgcn_s_waitcnt(kWait);
       asm volatile("s_barrier" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
-      la.issue(stA(sa), kt + 2, wave);
-      if constexpr (BST == 2) lb.issue(stB(sb), kt + 2, wave);
-      read(f0, stA(Stage<1 - SA>{}), stB(Stage<(SB + 1) % BST>{}), 0);
+      la.issue(stA(sa), kt + AST, wave);
+      if constexpr (BST != 3) lb.issue(stB(sb), kt + BST, wave);
+      read(f0, stA(Stage<(SA + 1) % AST>{}), stB(Stage<(SB + 1) % BST>{}), 0);
       mma(f1);
-      interleave<NM, NR, NA + (BST == 2 ? NB : 0)>();
+      interleave<NM, NR, NA + (BST != 3 ? NB : 0)>();
     };
     if (nk > 0) {
       la.issue(sa0, 0, wave);
@@ -460,7 +488,13 @@ grouped_kernel(const GroupedArgs P) {
       la.issue(sa1, 1, wave);
       lb.issue(sb1, 1, wave);
       if constexpr (BST == 3) lb.issue(sb2, 2, wave);
-      MOE_WAIT_VMCNT(NA + (BST - 1) * NB);
+      if constexpr (DEEP) {
+        la.issue(sa2, 2, wave);
+        lb.issue(sb2, 2, wave);
+        la.issue(sa3, 3, wave);
+        lb.issue(sb3, 3, wave);
+      }
+      MOE_WAIT_VMCNT((AST - 1) * NA + (BST - 1) * NB);
       asm volatile("s_barrier" ::: "memory");
       __builtin_amdgcn_sched_barrier(0);
       read(f0, sa0, sb0, 0);
@@ -474,6 +508,22 @@ grouped_kernel(const GroupedArgs P) {
           step(kt + 1, S1, S1, S0);
         }
         if (kt < nk) step(kt, S0, S0, S0);
+      } else if constexpr (DEEP) {
+        const Stage<3> S3{};
+        int kt = 0;
+        for (; kt + 4 <= nk; kt += 4) {
+          step(kt, S0, S0, S0);
+          step(kt + 1, S1, S1, S0);
+          step(kt + 2, S2, S2, S0);
+          step(kt + 3, S3, S3, S0);
+        }
+        if (kt < nk) {
+          step(kt, S0, S0, S0);
+          if (kt + 1 < nk) {
+            step(kt + 1, S1, S1, S0);
+            if (kt + 2 < nk) step(kt + 2, S2, S2, S0);
+          }
+        }
       } else {
         step(0, S0, S0, S1);
         // step kt reads A stage kt % 2 and B stage kt % 3

@@ -14,8 +14,7 @@ namespace moe {
 constexpr int kRestBlocks = 64;
 __global__ void __launch_bounds__(1024) grouped_tiles_kernel(const int32_t* __restrict__ offsets, int E, int R, int BM,
                                                              int2* __restrict__ ranges, TileRec* __restrict__ tiles,
-                                                             int32_t* __restrict__ n_mtiles,
-                                                             int32_t* __restrict__ counters, const RestRows rest) {
+                                                             int32_t* __restrict__ n_mtiles, const RestRows rest) {
   __shared__ int wmax[16], wsum[16];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   auto clamped = [&](int i) { return min(max(offsets[min(i, E)], 0), R); };
@@ -26,7 +25,6 @@ __global__ void __launch_bounds__(1024) grouped_tiles_kernel(const int32_t* __re
     if (lane >= d) v = max(v, o);
   }
   if (lane == 63) wmax[wave] = v;
-  if (blockIdx.x == 0 && tid < kGemmCounters) counters[tid] = 0;
   __syncthreads();
   for (int w = 0; w < wave; ++w) v = max(v, wmax[w]);
   if (blockIdx.x > 0) {
@@ -55,55 +53,119 @@ __global__ void __launch_bounds__(1024) grouped_tiles_kernel(const int32_t* __re
 hipError_t launch_grouped_tiles(const int32_t* offsets, int E, int R, int BM, const GroupedScratch& s,
                                 const RestRows& rest, hipStream_t st) {
   hipLaunchKernelGGL(grouped_tiles_kernel, dim3(rest.C && R > 0 ? 1 + kRestBlocks : 1), dim3(1024), 0, st, offsets, E, R,
-                     BM, s.ranges, s.tiles, s.n_mtiles, s.counters, rest);
+                     BM, s.ranges, s.tiles, s.n_mtiles, rest);
   return hipGetLastError();
 }
 
-#ifndef GT_BIG
-#define GT_BIG 2
-#endif
-#ifndef GT_BST
-#define GT_BST 3
-#endif
 template <int FORM, int OUT>
-static void launch_form(const GroupedArgs& a, int BM, int64_t grid, hipStream_t st) {
-  if (BM == 256) {
-#if GT_BIG == 1
-    hipLaunchKernelGGL((grouped_kernel<FORM, 256, 256, 2, 2, 1, OUT, GT_BST>), dim3((unsigned)grid), dim3(256), 0, st, a);
-#else
-    hipLaunchKernelGGL((grouped_kernel<FORM, 256, 256, 2, 4, 2, OUT, GT_BST>), dim3((unsigned)grid), dim3(512), 0, st, a);
-#endif
-  } else
-    hipLaunchKernelGGL((grouped_kernel<FORM, 128, 128, 2, 2, 2, OUT, 2>), dim3((unsigned)grid), dim3(256), 0, st, a);
+static void launch_form(const GroupedArgs& a, const GroupedPlan& plan, int64_t grid, hipStream_t st) {
+  const dim3 g((unsigned)grid);
+  if (plan.bm == 256)
+    hipLaunchKernelGGL((grouped_kernel<FORM, 256, 256, 2, 4, 2, OUT, 2, 3>), g, dim3(512), 0, st, a);
+  else if (plan.deep)
+    hipLaunchKernelGGL((grouped_kernel<FORM, 128, 128, 2, 2, 1, OUT, 4, 4>), g, dim3(256), 0, st, a);
+  else
+    hipLaunchKernelGGL((grouped_kernel<FORM, 128, 128, 2, 2, 2, OUT, 2, 2>), g, dim3(256), 0, st, a);
 }
 
-// Which tiles, from what the host knows (the rows' number, not how they spread).
-// 256-row tiles where an expert has 128 rows or more on average; else 128.
-int grouped_bm(int64_t R, int E) { return R >= (int64_t)E * 128 ? 256 : 128; }
-
+// Which tiles, from what the host knows (the rows' number, not their spread; an
+// expert's last M tile is taken as half used). us of a call, 256 x 256 tiles /
+// 128 x 128 tiles / the latter with four stages:
+//   rows product, R 20000, E 2, [640, 640] (237 big tiles)   22 / 26 / 37
+//   rows product, R 32768, E 128, [2048, 5120]              806 / 999 / 1101
+//   wgrad, R 8000, E 30, [504, 3000] (720 big tiles)         59 / 81 / 104
+//   wgrad, R 20000, E 2, [640, 640] (18 big, 50 small)        - / 100 / 62
+//   dgrad, R 2000, E 16, [1200, 400] (124 small tiles)        - / 15.8 / 13.2
+// So the big tile where its tiles come near the 256 CUs' number, else the small
+// one, with four stages while every workgroup has a CU to itself (more of them
+// then ask for more than the L2 gives: 0.25 us of MFMA a k tile, 32 KB).
+constexpr int64_t kBigTiles = 192, kDeepGrid = 256;
 // Grids of at most this many workgroups find their tiles in the offsets
-// (OffsetScan) and need no table.
+// (OffsetScan) and need no table: up to 128 experts, two to a lane (at 512
+// experts and 880 workgroups the table was 11 us faster).
 constexpr int64_t kScanGrid = 1024;
 constexpr int kScanExperts = 128;
 
+static void finish_plan(GroupedPlan& p, int E) {
+  p.deep = p.bm == 128 && p.grid <= kDeepGrid;
+  p.scan = p.grid <= kScanGrid && E <= kScanExperts;
+}
+
 GroupedPlan grouped_rows_plan(int64_t R, int E, int N) {
-  GroupedPlan p;
-  p.bm = grouped_bm(R, E);
-  p.mtiles = 0;
+  GroupedPlan p{};
+  const int64_t big = (R / 256 + std::min<int64_t>(R, E) / 2) * ((N + 255) / 256);
+  p.bm = R >= (int64_t)E * 128 && big >= kBigTiles ? 256 : 128;
   p.ntiles = (N + p.bm - 1) / p.bm;
   p.grid = grouped_max_tiles(R, E, p.bm) * p.ntiles;
-  p.scan = p.grid <= kScanGrid && E <= kScanExperts;
+  finish_plan(p, E);
   return p;
 }
 
-GroupedPlan grouped_wgrad_plan(int E, int M, int N) {
-  GroupedPlan p;
-  p.bm = (int64_t)E * ((M + 255) / 256) * ((N + 255) / 256) >= 256 ? 256 : 128;
+// A weight gradient of few tiles and many rows (less than half the CUs, 1024
+// rows) sums pieces of each expert's rows side by side, as many as give every
+// CU a workgroup, and joins them in row order: [640, 640] x 2 experts over
+// 20000 rows 62 us in one piece each. Pieces are multiples of a k tile, 256 rows or more.
+GroupedPlan grouped_wgrad_plan(int64_t R, int E, int M, int N) {
+  GroupedPlan p{};
+  p.bm = (int64_t)E * ((M + 255) / 256) * ((N + 255) / 256) >= kBigTiles ? 256 : 128;
   p.mtiles = (M + p.bm - 1) / p.bm;
   p.ntiles = (N + p.bm - 1) / p.bm;
-  p.grid = (int64_t)E * p.mtiles * p.ntiles;
-  p.scan = p.grid <= kScanGrid && E <= kScanExperts;
+  const int64_t tiles = (int64_t)p.mtiles * p.ntiles;
+  p.grid = E * tiles;
+  if (p.bm == 128 && p.grid <= kDeepGrid / 2 && R >= 1024 && E <= kScanExperts) {
+    const int64_t pieces = kDeepGrid / tiles;
+    p.split = (int)std::max<int64_t>(256, (R + pieces - 1) / pieces + 63) / 64 * 64;
+    p.pieces = grouped_max_tiles(R, E, p.split);
+    p.grid = p.pieces * tiles;
+  }
+  finish_plan(p, E);
+  if (p.split) p.deep = p.scan = true;
   return p;
+}
+
+size_t grouped_partial_bytes(const GroupedPlan& p, int M, int N) {
+  return p.split ? (size_t)p.pieces * M * N * sizeof(float) : 0;
+}
+
+// dW[e] = the sum of expert e's pieces, in row order (zero pieces: zeros), added
+// to what it holds if asked. A thread takes 4 elements.
+template <int OUT>
+__global__ void __launch_bounds__(256) wgrad_join_kernel(const float* __restrict__ partial, const GroupedArgs P,
+                                                         int64_t size, int blocks) {
+  const int lane = threadIdx.x & 63;
+  const int e = blockIdx.x / blocks;
+  const OffsetScan scan(P.offsets, P.E, P.R, lane);
+  int incl;
+  scan.tiles(P.split, incl);
+  int first = 0, n = 0, at = incl;
+  scan.each([&](int, int a, int b) { at -= (b - a + P.split - 1) / P.split; });
+  scan.each([&](int i, int a, int b) {
+    const int c = (b - a + P.split - 1) / P.split;
+    if (i == e) { first = at; n = c; }
+    at += c;
+  });
+  first = __builtin_amdgcn_readlane(first, e / scan.C);
+  n = __builtin_amdgcn_readlane(n, e / scan.C);
+  if (n == 0 && P.accumulate) return;
+  const int64_t i = ((int64_t)(blockIdx.x - e * blocks) * 256 + threadIdx.x) * 4;
+  if (i >= size) return;
+  const float* src = partial + first * size + i;
+  f32x4 s{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+  for (int k = 0; k < n; ++k) s += *reinterpret_cast<const f32x4*>(src + k * size);
+  if constexpr (OUT == EPI_F32) {
+    f32x4* dst = reinterpret_cast<f32x4*>(static_cast<float*>(P.C) + e * size + i);
+    if (P.accumulate) s += *dst;
+    *dst = s;
+  } else {
+    u32x2* dst = reinterpret_cast<u32x2*>(static_cast<uint16_t*>(P.C) + e * size + i);
+    if (P.accumulate) {
+      const u32x2 o = *dst;
+      s += f32x4{bf16_bits_to_f32(o.x & 0xFFFFu), bf16_bits_to_f32(o.x >> 16), bf16_bits_to_f32(o.y & 0xFFFFu),
+                 bf16_bits_to_f32(o.y >> 16)};
+    }
+    *dst = u32x2{cvt_pk_bf16(s[0], s[1]), cvt_pk_bf16(s[2], s[3])};
+  }
 }
 
 hipError_t launch_grouped_rows(const GroupedProduct& p, const GroupedPlan& plan, const GroupedScratch& s, bool rest,
@@ -125,10 +187,9 @@ hipError_t launch_grouped_rows(const GroupedProduct& p, const GroupedPlan& plan,
   a.R = (int)p.R;
   a.rest_blocks = plan.scan && rest ? kScanRestBlocks : 0;
   a.ntiles = plan.ntiles;
-  if (plan.grid > 0x7FFFFFFF) return hipErrorInvalidValue;
   const int64_t grid = plan.grid + a.rest_blocks;
-  if (p.transposed_b) launch_form<FORM_NN, EPI_BF16>(a, plan.bm, grid, st);
-  else launch_form<FORM_NT, EPI_BF16>(a, plan.bm, grid, st);
+  if (p.transposed_b) launch_form<FORM_NN, EPI_BF16>(a, plan, grid, st);
+  else launch_form<FORM_NT, EPI_BF16>(a, plan, grid, st);
   return hipGetLastError();
 }
 
@@ -151,9 +212,26 @@ hipError_t launch_grouped_wgrad(const GroupedProduct& p, int M, bool f32, bool a
   a.mtiles = plan.mtiles;
   a.ntiles = plan.ntiles;
   a.accumulate = accumulate;
-  if (plan.grid > 0x7FFFFFFF) return hipErrorInvalidValue;
-  if (f32) launch_form<FORM_TN, EPI_F32>(a, plan.bm, plan.grid, st);
-  else launch_form<FORM_TN, EPI_BF16>(a, plan.bm, plan.grid, st);
+  if (plan.split) {
+    GroupedArgs q = a;
+    q.split = plan.split;
+    q.C = s.partial;
+    q.ldc = p.N;
+    q.c_estride = (int64_t)M * p.N;
+    q.accumulate = 0;
+    launch_form<FORM_TN, EPI_F32>(q, plan, plan.grid, st);
+    const hipError_t err = hipGetLastError();
+    if (err != hipSuccess) return err;
+    a.split = plan.split;
+    const int64_t size = (int64_t)M * p.N;
+    const int blocks = (int)((size + 1023) / 1024);
+    const dim3 grid((unsigned)((int64_t)p.E * blocks));
+    if (f32) hipLaunchKernelGGL(wgrad_join_kernel<EPI_F32>, grid, dim3(256), 0, st, s.partial, a, size, blocks);
+    else hipLaunchKernelGGL(wgrad_join_kernel<EPI_BF16>, grid, dim3(256), 0, st, s.partial, a, size, blocks);
+    return hipGetLastError();
+  }
+  if (f32) launch_form<FORM_TN, EPI_F32>(a, plan, plan.grid, st);
+  else launch_form<FORM_TN, EPI_BF16>(a, plan, plan.grid, st);
   return hipGetLastError();
 }
 

@@ -10,7 +10,7 @@ struct GroupedScratch {
   int2* ranges;        // [E] rows of each expert
   int4* tiles;         // [grouped_max_tiles] M tile table
   int32_t* n_mtiles;   // [1]
-  int32_t* counters;   // [kGemmCounters] zeroed by launch_grouped_tiles
+  float* partial;      // sums of the pieces of a split weight gradient
 };
 
 // M tiles that R rows in E experts can need
@@ -31,11 +31,15 @@ struct GroupedProduct {
 struct GroupedPlan {
   int bm, mtiles, ntiles;
   int64_t grid;
+  int64_t pieces;      // split: the most pieces the rows can make
+  int split;           // wgrad: rows of a piece, 0 for whole experts
+  bool deep;           // four LDS stages
   bool scan;           // the kernel finds its tiles itself; else it needs launch_grouped_tiles
 };
 constexpr int kScanRestBlocks = 16;   // workgroups that zero the rows of no expert, without a table
 GroupedPlan grouped_rows_plan(int64_t R, int E, int N);
-GroupedPlan grouped_wgrad_plan(int E, int M, int N);
+GroupedPlan grouped_wgrad_plan(int64_t R, int E, int M, int N);
+size_t grouped_partial_bytes(const GroupedPlan& p, int M, int N);
 
 // Output whose rows of no expert are to be zeroed (C null: none).
 struct RestRows {
@@ -67,7 +71,6 @@ struct Fp8Args {
   int E, rest_blocks;
   int ntiles;
 };
-GroupedPlan fp8_plan(int64_t R, int E, int N);
 hipError_t launch_fp8_rows(const uint16_t* x, int64_t R, int K, int64_t ldx, uint8_t* codes, float* scales,
                            hipStream_t st);
 hipError_t launch_fp8_blocks(const uint16_t* w, int64_t count, int N, int K, uint8_t* codes, float* scales,

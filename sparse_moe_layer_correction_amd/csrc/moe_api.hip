@@ -351,7 +351,7 @@ const char* moe_status_string(int status) {
       return "invalid argument (null pointer, non-positive size, K > E, bad row length or bad expert groups)";
     case MOE_ERR_UNSUPPORTED:
       return "unsupported size (H, L, I, Is must be multiples of 64; E <= 1024; K <= 64; T*K < 2^31; "
-             "2*T*L < 2^32; n_group <= 64)";
+             "2*T*L < 2^32; n_group <= 64; grouped products: N, K and strides multiples of 8, 8-bit K of 16)";
     case MOE_ERR_WORKSPACE: return "workspace null, too small or not 256-byte aligned";
     case MOE_ERR_HIP: return "HIP launch error";
     case MOE_ERR_TOO_LARGE:

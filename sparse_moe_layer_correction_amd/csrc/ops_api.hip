@@ -18,12 +18,14 @@ constexpr size_t kAlign = 256;
 size_t align_up(size_t x) { return (x + kAlign - 1) & ~(kAlign - 1); }
 int hip_status(hipError_t e) { return e == hipSuccess ? MOE_OK : MOE_ERR_HIP; }
 bool ws_ok(const void* ws, size_t have, size_t need) {
+  if (need == 0) return true;
   return ws != nullptr && have >= need && (reinterpret_cast<uintptr_t>(ws) % kAlign) == 0;
 }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// the smallest M tile, which needs the longest table
-constexpr int kMinBM = 64;
+// a grid's threads are counted in 32 bits; workgroups have up to 512
+constexpr int64_t kMaxGrid = (int64_t)1 << 23;
+constexpr int64_t kMaxBlocks = (int64_t)1 << 28;   // 16 to a workgroup of 256 threads
 constexpr int64_t kMaxStride = (int64_t)1 << 22;   // 256 rows of 2 bytes stay below 2 GiB
 
 // dims with the dense strides filled in
@@ -43,25 +45,31 @@ int grouped_dims(const moe_grouped_dims* in, moe_grouped_dims* d) {
   if (d->E > kMaxExperts || d->R > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
   if ((d->N | d->K) % 8 || (d->ldx | d->ldy | d->ldw | d->w_stride | d->lddx) % 8) return MOE_ERR_UNSUPPORTED;
   if (std::max(std::max(d->ldx, d->ldy), std::max(d->ldw, d->lddx)) >= kMaxStride) return MOE_ERR_UNSUPPORTED;
-  // tiles of the three products, counted with the smallest tile
-  const int64_t nt = (d->N + kMinBM - 1) / kMinBM, kt = (d->K + kMinBM - 1) / kMinBM;
-  if (grouped_max_tiles(d->R, d->E, kMinBM) * std::max(nt, kt) > 0x7FFFFFFF || (int64_t)d->E * nt * kt > 0x7FFFFFFF)
-    return MOE_ERR_UNSUPPORTED;
+  for (int n : {d->N, d->K})
+    if (grouped_rows_plan(d->R, d->E, n).grid >= kMaxGrid) return MOE_ERR_UNSUPPORTED;
+  if (grouped_wgrad_plan(d->R, d->E, d->N, d->K).grid >= kMaxGrid) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
+// Workspace of a call: the tile table of the products that need one, and what the call adds.
 struct GroupedLayout {
-  size_t counters, n_mtiles, ranges, tiles, total;
+  size_t n_mtiles, ranges, tiles, partial, codes, scales, total;
 };
 
-GroupedLayout grouped_layout(const moe_grouped_dims& d) {
+GroupedLayout grouped_layout(const moe_grouped_dims& d, int table_bm, size_t partial, bool quantise) {
   GroupedLayout l{};
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o = align_up(o + bytes); return at; };
-  l.counters = take(kGemmCounters * 4);
-  l.n_mtiles = take(4);
-  l.ranges = take((size_t)d.E * 8);
-  l.tiles = take((size_t)grouped_max_tiles(d.R, d.E, kMinBM) * 16);
+  if (table_bm > 0) {
+    l.n_mtiles = take(4);
+    l.ranges = take((size_t)d.E * 8);
+    l.tiles = take((size_t)grouped_max_tiles(d.R, d.E, table_bm) * 16);
+  }
+  if (partial > 0) l.partial = take(partial);
+  if (quantise) {
+    l.codes = take((size_t)d.R * d.K);
+    l.scales = take((size_t)((d.K + 127) / 128) * d.R * 4);
+  }
   l.total = o;
   return l;
 }
@@ -69,7 +77,28 @@ GroupedLayout grouped_layout(const moe_grouped_dims& d) {
 GroupedScratch grouped_scratch(const GroupedLayout& l, void* ws) {
   char* p = static_cast<char*>(ws);
   return GroupedScratch{reinterpret_cast<int2*>(p + l.ranges), reinterpret_cast<int4*>(p + l.tiles),
-                        reinterpret_cast<int32_t*>(p + l.n_mtiles), reinterpret_cast<int32_t*>(p + l.counters)};
+                        reinterpret_cast<int32_t*>(p + l.n_mtiles), reinterpret_cast<float*>(p + l.partial)};
+}
+
+int table_of(const GroupedPlan& p) { return p.scan ? 0 : p.bm; }
+
+GroupedLayout forward_layout(const moe_grouped_dims& d, const GroupedPlan& p, bool quantise = false) {
+  return grouped_layout(d, d.R > 0 ? table_of(p) : 0, 0, quantise);
+}
+
+struct GradPlans {
+  GroupedPlan rows, wgrad;
+  int table_bm;              // of the one table both use (the rows product's tiles; the gradient takes its ranges)
+};
+
+GradPlans grad_plans(const moe_grouped_dims& d, bool dx, bool dw) {
+  GradPlans g{grouped_rows_plan(d.R, d.E, d.K), grouped_wgrad_plan(d.R, d.E, d.N, d.K), 0};
+  if ((dx && !g.rows.scan) || (dw && !g.wgrad.scan)) g.table_bm = g.rows.bm;
+  return g;
+}
+
+GroupedLayout grad_layout(const moe_grouped_dims& d, const GradPlans& g, bool dw) {
+  return grouped_layout(d, g.table_bm, dw ? grouped_partial_bytes(g.wgrad, d.N, d.K) : 0, false);
 }
 
 }  // namespace
@@ -79,7 +108,10 @@ extern "C" {
 size_t moe_grouped_workspace_bytes(const moe_grouped_dims* dims) {
   moe_grouped_dims d;
   if (grouped_dims(dims, &d) != MOE_OK) return 0;
-  return grouped_layout(d).total;
+  const GradPlans g = grad_plans(d, true, true);
+  const size_t q = d.K % 16 == 0 ? forward_layout(d, grouped_rows_plan(d.R, d.E, d.N), true).total : 0;
+  return std::max(std::max(forward_layout(d, grouped_rows_plan(d.R, d.E, d.N)).total, q),
+                  std::max(grad_layout(d, g, true).total, kAlign));
 }
 
 int moe_grouped_matmul(const moe_grouped_dims* dims, const uint16_t* x, const uint16_t* w, const int32_t* offsets,
@@ -89,11 +121,11 @@ int moe_grouped_matmul(const moe_grouped_dims* dims, const uint16_t* x, const ui
   if (st != MOE_OK) return st;
   if (!w || !offsets || (d.R > 0 && (!x || !y))) return MOE_ERR_INVALID;
   if (!aligned16(x) || !aligned16(w) || !aligned16(y)) return MOE_ERR_INVALID;
-  const GroupedLayout l = grouped_layout(d);
+  const GroupedPlan plan = grouped_rows_plan(d.R, d.E, d.N);
+  const GroupedLayout l = forward_layout(d, plan);
   if (!ws_ok(ws, ws_bytes, l.total)) return MOE_ERR_WORKSPACE;
   if (d.R == 0) return MOE_OK;
   const GroupedScratch s = grouped_scratch(l, ws);
-  const GroupedPlan plan = grouped_rows_plan(d.R, d.E, d.N);
   const RestRows rest{d.zero_rest ? y : nullptr, d.ldy, d.N};
   if (!plan.scan && launch_grouped_tiles(offsets, d.E, (int)d.R, plan.bm, s, rest, stream) != hipSuccess)
     return MOE_ERR_HIP;
@@ -111,13 +143,14 @@ int moe_grouped_matmul_grad(const moe_grouped_dims* dims, const uint16_t* dy, co
   if (dw_dtype != MOE_BF16 && dw_dtype != MOE_FP32) return MOE_ERR_INVALID;
   if (d.R > 0 && (!dy || (dx && !w) || (dw && !x))) return MOE_ERR_INVALID;
   if (!aligned16(dy) || !aligned16(x) || !aligned16(w) || !aligned16(dx) || !aligned16(dw)) return MOE_ERR_INVALID;
-  const GroupedLayout l = grouped_layout(d);
+  const bool run_dx = dx && d.R > 0;
+  const GradPlans plans = grad_plans(d, run_dx, dw != nullptr);
+  const GroupedPlan &rows = plans.rows, &wg = plans.wgrad;
+  const GroupedLayout l = grad_layout(d, plans, dw != nullptr);
   if (!ws_ok(ws, ws_bytes, l.total)) return MOE_ERR_WORKSPACE;
   const GroupedScratch s = grouped_scratch(l, ws);
-  const GroupedPlan rows = grouped_rows_plan(d.R, d.E, d.K), wg = grouped_wgrad_plan(d.E, d.N, d.K);
-  const bool run_dx = dx && d.R > 0;
   const RestRows rest{run_dx && !rows.scan && d.zero_rest ? dx : nullptr, d.lddx, d.K};
-  if ((run_dx && !rows.scan) || (dw && !wg.scan))
+  if (plans.table_bm > 0)
     if (launch_grouped_tiles(offsets, d.E, (int)d.R, rows.bm, s, rest, stream) != hipSuccess) return MOE_ERR_HIP;
   if (run_dx) {
     const GroupedProduct p{dy, w, dx, d.ldy, d.ldw, d.lddx, d.w_stride, d.R, d.E, d.K, d.N, true, offsets};
@@ -136,7 +169,7 @@ int moe_quantize_fp8_rows(const uint16_t* x, int64_t R, int32_t K, int64_t ldx, 
   if (R < 0 || K <= 0 || ldx < 0) return MOE_ERR_INVALID;
   if (ldx == 0) ldx = K;
   if (ldx < K || (R > 0 && (!x || !codes || !scales)) || !aligned16(x) || !aligned16(codes)) return MOE_ERR_INVALID;
-  if (K % 8 || ldx % 8 || R > (int64_t)0x7FFFFFFF / ((K + 127) / 128)) return MOE_ERR_UNSUPPORTED;
+  if (K % 8 || ldx % 8 || R >= kMaxBlocks / ((K + 127) / 128)) return MOE_ERR_UNSUPPORTED;
   return hip_status(launch_fp8_rows(x, R, K, ldx, codes, scales, stream));
 }
 
@@ -145,26 +178,40 @@ int moe_quantize_fp8_blocks(const uint16_t* w, int64_t count, int32_t N, int32_t
   if (count < 0 || N <= 0 || K <= 0) return MOE_ERR_INVALID;
   if ((count > 0 && (!w || !codes || !scales)) || !aligned16(w) || !aligned16(codes)) return MOE_ERR_INVALID;
   if (K % 8 || (int64_t)N * K > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
-  if (count > (int64_t)0x7FFFFFFF / ((int64_t)((N + 127) / 128) * ((K + 127) / 128))) return MOE_ERR_UNSUPPORTED;
+  if (count >= (kMaxGrid * 2) / ((int64_t)((N + 127) / 128) * ((K + 127) / 128))) return MOE_ERR_UNSUPPORTED;
   return hip_status(launch_fp8_blocks(w, count, N, K, codes, scales, stream));
 }
 
-int moe_grouped_matmul_fp8(const moe_grouped_dims* dims, const uint8_t* xq, const float* xs, const uint8_t* wq,
-                           const float* w_scale, const int32_t* offsets, uint16_t* y, void* ws, size_t ws_bytes,
-                           hipStream_t stream) {
+}  // extern "C"
+
+namespace {
+
+// The 8-bit product of checked dims; codes and scales of the rows given, or x (bf16) to quantise into the workspace.
+int fp8_impl(const moe_grouped_dims* dims, bool quantise, const uint16_t* x, const uint8_t* xq, const float* xs, const uint8_t* wq,
+             const float* w_scale, const int32_t* offsets, uint16_t* y, void* ws, size_t ws_bytes,
+             hipStream_t stream) {
   if (dims == nullptr) return MOE_ERR_INVALID;
   moe_grouped_dims d = *dims;
-  d.ldx = d.ldw = d.w_stride = d.lddx = 0;              // codes are dense
+  d.ldw = d.w_stride = d.lddx = 0;                      // codes are dense
+  if (!quantise) d.ldx = 0;
   const int st = grouped_dims(&d, &d);
   if (st != MOE_OK) return st;
   if (d.K % 16) return MOE_ERR_UNSUPPORTED;
-  if (!wq || !w_scale || !offsets || (d.R > 0 && (!xq || !xs || !y))) return MOE_ERR_INVALID;
-  if (!aligned16(xq) || !aligned16(wq) || !aligned16(y)) return MOE_ERR_INVALID;
-  const GroupedLayout l = grouped_layout(d);
+  if (quantise && d.R >= kMaxBlocks / ((d.K + 127) / 128)) return MOE_ERR_UNSUPPORTED;
+  if (!wq || !w_scale || !offsets || (d.R > 0 && (!y || (quantise ? !x : !xq || !xs)))) return MOE_ERR_INVALID;
+  if (!aligned16(x) || !aligned16(xq) || !aligned16(wq) || !aligned16(y)) return MOE_ERR_INVALID;
+  const GroupedPlan plan = grouped_rows_plan(d.R, d.E, d.N);
+  const GroupedLayout l = forward_layout(d, plan, quantise);
   if (!ws_ok(ws, ws_bytes, l.total)) return MOE_ERR_WORKSPACE;
   if (d.R == 0) return MOE_OK;
   const GroupedScratch s = grouped_scratch(l, ws);
-  const GroupedPlan plan = fp8_plan(d.R, d.E, d.N);
+  if (quantise) {
+    uint8_t* codes = static_cast<uint8_t*>(ws) + l.codes;
+    float* scales = reinterpret_cast<float*>(static_cast<char*>(ws) + l.scales);
+    if (launch_fp8_rows(x, d.R, d.K, d.ldx, codes, scales, stream) != hipSuccess) return MOE_ERR_HIP;
+    xq = codes;
+    xs = scales;
+  }
   const RestRows rest{!plan.scan && d.zero_rest ? y : nullptr, d.ldy, d.N};
   if (!plan.scan && launch_grouped_tiles(offsets, d.E, (int)d.R, plan.bm, s, rest, stream) != hipSuccess)
     return MOE_ERR_HIP;
@@ -187,6 +234,22 @@ int moe_grouped_matmul_fp8(const moe_grouped_dims* dims, const uint8_t* xq, cons
   a.rest_blocks = plan.scan && d.zero_rest ? kScanRestBlocks : 0;
   a.ntiles = plan.ntiles;
   return hip_status(launch_grouped_fp8(a, plan, stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+int moe_grouped_matmul_fp8(const moe_grouped_dims* dims, const uint8_t* xq, const float* xs, const uint8_t* wq,
+                           const float* w_scale, const int32_t* offsets, uint16_t* y, void* ws, size_t ws_bytes,
+                           hipStream_t stream) {
+  return fp8_impl(dims, false, nullptr, xq, xs, wq, w_scale, offsets, y, ws, ws_bytes, stream);
+}
+
+int moe_grouped_matmul_fp8_rows(const moe_grouped_dims* dims, const uint16_t* x, const uint8_t* wq,
+                                const float* w_scale, const int32_t* offsets, uint16_t* y, void* ws, size_t ws_bytes,
+                                hipStream_t stream) {
+  return fp8_impl(dims, true, x, nullptr, nullptr, wq, w_scale, offsets, y, ws, ws_bytes, stream);
 }
 
 }  // extern "C"

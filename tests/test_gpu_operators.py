@@ -511,10 +511,70 @@ def test_other_streams():
         assert all(torch.equal(a, b) for a, b in zip(want, got))
 
 
-def test_workspace_of_the_caller():
-    R, E, N, K, counts = 300, 5, 136, 72, [129, 0, 128, 1, 42]
-    x, w, o = rnd((R, K), 1), rnd((E, N, K), 2), offs(counts)
-    ws = torch.full((M.grouped_workspace_bytes(R, E, N, K),), 255, dtype=torch.uint8, device="cuda")
-    assert torch.equal(M.grouped_matmul(x, w, o, ws=ws), M.grouped_matmul(x, w, o))
+@pytest.mark.parametrize("R,E,N,K", [(300, 5, 136, 80), (1000, 200, 136, 80), (5000, 3, 136, 80)])
+def test_workspace_of_the_caller(R, E, N, K):
+    """Calls without a table, with one, and with the pieces of a split gradient, in a workspace full of junk."""
+    x, w, dy = rnd((R, K), 1), rnd((E, N, K), 2), rnd((R, N), 3)
+    o = offs(np.random.default_rng(4).multinomial(R, np.ones(E) / E))
+    wq, sw = M.quantize_fp8_blocks(w)
+    calls = (lambda ws: (M.grouped_matmul(x, w, o, ws=ws),), lambda ws: M.grouped_matmul_grad(dy, x, w, o, ws=ws),
+             lambda ws: (M.grouped_matmul_fp8(x, wq, sw, o, ws=ws),))
+    for call in calls:
+        ws = torch.full((M.grouped_workspace_bytes(R, E, N, K) + 256,), 255, dtype=torch.uint8, device="cuda")
+        for a, b in zip(call(ws[:-256]), call(None)):
+            assert torch.equal(a, b)
+        assert (ws[-256:] == 255).all()
     with pytest.raises(M.MoEError):
-        M.grouped_matmul(x, w, o, ws=ws[:-256])
+        M.grouped_matmul_fp8(x, wq, sw, o, ws=ws[:256])
+    with pytest.raises(M.MoEError):
+        M.grouped_matmul_fp8(x, wq, sw, o, ws=ws[1:])
+
+
+def ragged(R, E, seed, holes=0):
+    rng = np.random.default_rng(seed)
+    p = rng.random(E)
+    p[rng.permutation(E)[:holes]] = 0
+    return rng.multinomial(R, p / p.sum()).tolist()
+
+
+# every kind of plan: with a tile table (E > 128), big tiles with short last ones, four stages, split gradients
+PLANS = [
+    (2000, 200, 136, 80, ragged(2000, 200, 1, 60)),
+    (9000, 40, 1032, 272, ragged(9000, 40, 2, 4)),
+    (13000, 12, 1032, 528, [64, 1, 128, 129, 192, 193, 256, 257, 0, 5000, 3000, 3780]),
+    (6000, 3, 136, 272, [0, 5999, 1]),
+    (5000, 128, 8, 16, ragged(5000, 128, 3, 50)),
+    (1500, 1, 200, 336, [1500]),
+    (40000, 2, 264, 144, [33000, 7000]),
+    (30000, 7, 520, 2064, ragged(30000, 7, 4)),
+]
+
+
+@pytest.mark.parametrize("R,E,N,K,counts", PLANS)
+def test_every_plan(R, E, N, K, counts):
+    """The larger plans, against 64-bit sums on the GPU."""
+    x, w, dy, o = rnd((R, K), 3), rnd((E, N, K), 4, K ** -0.5), rnd((R, N), 5), offs(counts)
+    X, Wt, G = x.double(), w.double(), dy.double()
+    y = M.grouped_matmul(x, w, o)
+    dx, dw = M.grouped_matmul_grad(dy, x, w, o, dw_dtype=F32)
+    dwb = M.grouped_matmul_grad(dy, x, w, o, need_dx=False)[1]
+    wq, sw = M.quantize_fp8_blocks(w)
+    y8 = M.grouped_matmul_fp8(x, wq, sw, o)
+    q, sx = M.quantize_fp8_rows(x)                            # (pinned against the definition above)
+    XV = q.view(torch.float8_e4m3fn).double() * sx.double().t().repeat_interleave(128, 1)[:, :K]
+    for e, (a, b) in enumerate(ranges(o, R)):
+        ops = lambda u, v: ((u @ v).cpu(), (u.abs() @ v.abs()).cpu())
+        ref, s = ops(G[a:b].t().contiguous(), X[a:b])
+        check(dw[e], ref, s, b - a, F32)
+        check(dwb[e], ref, s, b - a, BF)
+        if a == b:
+            continue
+        check(y[a:b], *ops(X[a:b], Wt[e].t().contiguous()), K, BF)
+        check(dx[a:b], *ops(G[a:b], Wt[e]), N, BF)
+        wv = wq[e].view(torch.float8_e4m3fn).double() * sw[e].double().repeat_interleave(128, 0)[:N].repeat_interleave(128, 1)[:, :K]
+        ref, s = ops(XV[a:b], wv.t().contiguous())
+        loss = 7 * 2.0 ** -13 * (XV[a:b].abs().view(b - a, K // 8, 8).amax(2) @ wv.abs().view(N, K // 8, 8).amax(2).t())
+        check(y8[a:b], ref, s, K + 2 * ((K + 127) // 128), BF, loss.cpu())
+    keep = dw.clone()
+    M.grouped_matmul_grad(dy, x, w, o, need_dx=False, dw=dw, accumulate=True)
+    assert torch.allclose(dw, 2 * keep, rtol=2.0 ** -22, atol=0)

@@ -28,7 +28,7 @@ REFUSED = [
     (dict(ldx=-128), -1),
     (dict(N=60), -2), (dict(K=100), -2), (dict(ldx=132), -2), (dict(w_stride=64 * 128 + 4), -2),
     (dict(E=1025), -2), (dict(R=1 << 31), -2), (dict(ldx=1 << 22), -2),
-    (dict(R=(1 << 31) - 1, N=1 << 20), -2), (dict(E=1024, N=1 << 17, K=1 << 17), -2),
+    (dict(R=(1 << 31) - 1, N=1 << 20), -2), (dict(E=1024, N=1 << 15, K=1 << 15), -2),
 ]
 
 
@@ -54,9 +54,17 @@ def test_grouped_pointers(lib):
             a[i] = 264
             assert f(d, *a, 256, n, None) == -1
     assert f(None, 256, 256, 256, 256, 256, n, None) == -1
-    assert f(d, 256, 256, 256, 256, None, n, None) == -3
-    assert f(d, 256, 256, 256, 256, 128, n, None) == -3
-    assert f(d, 256, 256, 256, 256, 256, n - 1, None) == -3
+    big = dims(E=200, R=10000)                     # needs a tile table
+    bn = lib.moe_grouped_workspace_bytes(big)
+    for ws, have in ((None, bn), (128, bn), (256, 1024)):
+        assert f(big, 256, 256, 256, 256, ws, have, None) == -3
+        assert g(big, 256, 256, 256, 256, 256, 256, 0, 0, ws, have, None) == -3
+        assert q(big, *[256] * 6, ws, have, None) == -3
+    # bf16 rows are quantised into the workspace
+    assert lib.moe_grouped_matmul_fp8_rows(d, 256, 256, 256, 256, 256, 256, 100 * 128 - 1, None) == -3
+    assert lib.moe_grouped_matmul_fp8_rows(d, 256, 256, 256, 256, 256, None, 0, None) == -3
+    # a weight gradient split over the rows keeps its pieces there
+    assert g(dims(R=4096, E=1), 256, 256, 256, 256, None, 256, 0, 0, None, 0, None) == -3
     assert g(d, None, 256, 256, 256, 256, 256, 0, 0, 256, n, None) == -1
     assert g(d, 256, None, 256, 256, 256, 256, 0, 0, 256, n, None) == -1      # dw needs x
     assert g(d, 256, 256, None, 256, 256, 256, 0, 0, 256, n, None) == -1      # dx needs w
@@ -64,13 +72,18 @@ def test_grouped_pointers(lib):
     assert g(d, 256, 256, 256, 256, None, None, 0, 0, 256, n, None) == -1     # nothing to compute
     assert g(d, 256, 256, 256, 256, 256, 256, 2, 0, 256, n, None) == -1       # unknown type
     assert g(d, 256, 256, 256, 256, 264, 256, 0, 0, 256, n, None) == -1
-    assert g(d, 256, 256, 256, 256, 256, 256, 0, 0, 256, n - 1, None) == -3
     for i in range(6):
         a = [256] * 6
         a[i] = None
         assert q(d, *a, 256, n, None) == -1
     assert q(dims(K=136), *[256] * 6, 256, 1 << 40, None) == -2               # K a multiple of 16
-    assert q(d, *[256] * 6, 256, n - 1, None) == -3
+    r = lib.moe_grouped_matmul_fp8_rows
+    for i in range(5):
+        a = [256] * 5
+        a[i] = None
+        assert r(d, *a, 256, n, None) == -1
+    assert r(dims(ldx=120), *[256] * 5, 256, n, None) == -1
+    assert r(dims(R=(1 << 31) - 1, K=4096), *[256] * 5, 256, 1 << 50, None) == -2
 
 
 def test_quantisers(lib):
@@ -82,14 +95,14 @@ def test_quantisers(lib):
     assert r(256, 4, 64, 0, 264, 256, None) == -1
     assert r(256, 4, 60, 0, 256, 256, None) == -2
     assert r(256, 4, 64, 68, 256, 256, None) == -2
-    assert r(256, 1 << 31, 64, 0, 256, 256, None) == -2
+    assert r(256, 1 << 28, 64, 0, 256, 256, None) == -2
     assert b(256, -1, 64, 64, 256, 256, None) == -1
     assert b(256, 1, 64, 0, 256, 256, None) == -1
     assert b(256, 1, 64, 64, None, 256, None) == -1
     assert b(264, 1, 64, 64, 256, 256, None) == -1
     assert b(256, 1, 64, 60, 256, 256, None) == -2
     assert b(256, 1, 1 << 16, 1 << 15, 256, 256, None) == -2
-    assert b(256, 1 << 31, 8, 8, 256, 256, None) == -2
+    assert b(256, 1 << 24, 8, 8, 256, 256, None) == -2
 
 
 def tensors(*spec):
