@@ -817,24 +817,28 @@ def _grad_table(grads, out):
         raise ValueError(f"out must hold one tensor for each of the {len(grads)} gradients, got {len(outs)}")
     if not grads:
         raise ValueError("grads must hold at least one tensor")
-    kinds = {torch.bfloat16: 0, torch.float32: 1}
-    index = grads[0].get_device() if isinstance(grads[0], torch.Tensor) else -1
+    Tensor, bf16, fp32 = torch.Tensor, torch.bfloat16, torch.float32
+    index = grads[0].get_device() if isinstance(grads[0], Tensor) else -1
     words = []                       # four 64-bit words an entry: grad, out, n, dtype (and its padding)
-    for i, (g, o) in enumerate(zip(grads, outs)):
-        if not isinstance(g, torch.Tensor) or g.dtype not in kinds:
-            raise TypeError(f"gradient {i} must be a bf16 or fp32 torch tensor")
-        if index < 0 or g.get_device() != index:
+    for i, g in enumerate(grads):
+        if not isinstance(g, Tensor):
+            raise TypeError(f"gradient {i} must be a torch tensor")
+        dt = g.dtype
+        if dt is not bf16 and dt is not fp32:
+            raise TypeError(f"gradient {i} must be bf16 or fp32, got {dt}")
+        if g.get_device() != index or index < 0:
             raise ValueError(f"gradient {i} must be on the GPU of the first one, got {g.device}")
         if not g.is_contiguous():
             raise ValueError(f"gradient {i} must be contiguous")
-        n, at = g.numel(), g.data_ptr()
-        if o is g:
-            words += (at, 0, n, kinds[g.dtype])
-            continue
-        if not isinstance(o, torch.Tensor) or o.dtype != g.dtype or o.numel() != n or o.get_device() != index \
-                or not o.is_contiguous():
-            raise ValueError(f"out {i} must be a contiguous {g.dtype} tensor of {n} elements on {g.device}")
-        words += (at, o.data_ptr(), n, kinds[g.dtype])
+        n = g.numel()
+        o = outs[i]
+        at = 0
+        if o is not g:
+            if not isinstance(o, Tensor) or o.dtype is not dt or o.numel() != n or o.get_device() != index \
+                    or not o.is_contiguous():
+                raise ValueError(f"out {i} must be a contiguous {dt} tensor of {n} elements on {g.device}")
+            at = o.data_ptr()
+        words += (g.data_ptr(), at, n, 0 if dt is bf16 else 1)
     raw = (ctypes.c_int64 * len(words))(*words)
     return ctypes.cast(raw, ctypes.POINTER(_GradTensor)), raw, len(grads), grads[0].device
 

@@ -36,7 +36,8 @@ __device__ __forceinline__ double sq2(uint32_t w) {
 }
 
 // the table entry that holds chunk c: the last one that starts at or before it
-__device__ __forceinline__ int grad_entry(const GradTable& t, int c) {
+template <int SIZE>
+__device__ __forceinline__ int grad_entry(const GradTableOf<SIZE>& t, int c) {
   int lo = 0, hi = t.count - 1;
   while (lo < hi) {
     const int mid = (lo + hi + 1) >> 1;
@@ -53,7 +54,9 @@ __device__ __forceinline__ int head_of(const T* p, int n) {
   return min(mis, n);
 }
 
-__global__ void __launch_bounds__(kGradThreads) grad_sumsq_kernel(const GradTable t, double* __restrict__ partial) {
+template <int SIZE>
+__global__ void __launch_bounds__(kGradThreads) grad_sumsq_kernel(const GradTableOf<SIZE> t,
+                                                                  double* __restrict__ partial) {
   __shared__ double part[kGradThreads / kWave];
   double s = 0.0;
   for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
@@ -86,24 +89,34 @@ __global__ void __launch_bounds__(kGradThreads) grad_sumsq_kernel(const GradTabl
   if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
 
-// partials -> norm and the factor the gradients take
-__global__ void __launch_bounds__(1024) grad_norm_kernel(const double* __restrict__ partial, int n, double max_norm,
-                                                         float* __restrict__ norm, double* __restrict__ factor) {
-  __shared__ double part[16];
+// the sum of a call's partials, the same in every workgroup that takes it
+template <int THREADS>
+__device__ __forceinline__ double sum_partials(const double* partial, int n, double* part) {
   double s = 0.0;
-  for (int i = threadIdx.x; i < n; i += 1024) s += partial[i];
-  s = block_sum_f64(s, part);
-  if (threadIdx.x == 0) {
-    const double v = __builtin_sqrt(s);
-    *norm = (float)v;
-    // a norm that is not finite leaves the gradients as they are
-    if (factor != nullptr) *factor = v > max_norm && v < __builtin_inf() ? max_norm / v : 1.0;
-  }
+  for (int i = threadIdx.x; i < n; i += THREADS) s += partial[i];
+  return block_sum_f64(s, part);
 }
 
-__global__ void __launch_bounds__(kGradThreads) grad_scale_kernel(const GradTable t, const double* __restrict__ factor) {
-  const double f = *factor;
-  for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+__global__ void __launch_bounds__(1024) grad_norm_kernel(const double* __restrict__ partial, int n,
+                                                         float* __restrict__ norm) {
+  __shared__ double part[16];
+  const double s = sum_partials<1024>(partial, n, part);
+  if (threadIdx.x == 0) *norm = (float)__builtin_sqrt(s);
+}
+
+// Every workgroup sums the partials itself (16 KB, from the L2): no launch
+// between the two passes. The chunks are walked from the last to the first, as
+// the end of what the first pass read is what the caches still hold.
+template <int SIZE>
+__global__ void __launch_bounds__(kGradThreads) grad_scale_kernel(const GradTableOf<SIZE> t,
+                                                                  const double* __restrict__ partial, int np,
+                                                                  double max_norm, float* __restrict__ norm_out) {
+  __shared__ double part[kGradThreads / kWave];
+  const double norm = __builtin_sqrt(sum_partials<kGradThreads>(partial, np, part));
+  if (norm_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
+  // a norm that is not finite leaves the gradients as they are
+  const double f = norm > max_norm && norm < __builtin_inf() ? max_norm / norm : 1.0;
+  for (int c = t.chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
     const int i = grad_entry(t, c);
     if (f == 1.0 && t.src[i] == t.dst[i]) continue;      // in place and nothing to scale
     const int64_t at = (int64_t)(c - t.first[i]) * kGradChunk;
@@ -139,17 +152,40 @@ __global__ void __launch_bounds__(kGradThreads) grad_scale_kernel(const GradTabl
   }
 }
 
+static GradTableOf<kGradShortTable> short_table(const GradTable& t) {
+  GradTableOf<kGradShortTable> s{};
+  for (int i = 0; i < t.count; ++i) {
+    s.src[i] = t.src[i];
+    s.dst[i] = t.dst[i];
+    s.n[i] = t.n[i];
+    s.first[i] = t.first[i];
+  }
+  s.f32[0] = t.f32[0];
+  s.count = t.count;
+  s.chunks = t.chunks;
+  return s;
+}
+
 hipError_t launch_grad_sumsq(const GradTable& t, int blocks, double* partial, hipStream_t st) {
-  hipLaunchKernelGGL(grad_sumsq_kernel, dim3(blocks), dim3(kGradThreads), 0, st, t, partial);
+  if (t.count <= kGradShortTable)
+    hipLaunchKernelGGL(grad_sumsq_kernel<kGradShortTable>, dim3(blocks), dim3(kGradThreads), 0, st, short_table(t),
+                       partial);
+  else
+    hipLaunchKernelGGL(grad_sumsq_kernel<kGradTableSize>, dim3(blocks), dim3(kGradThreads), 0, st, t, partial);
   return hipGetLastError();
 }
-hipError_t launch_grad_norm(const double* partial, int n, double max_norm, float* norm, double* factor,
-                            hipStream_t st) {
-  hipLaunchKernelGGL(grad_norm_kernel, dim3(1), dim3(1024), 0, st, partial, n, max_norm, norm, factor);
+hipError_t launch_grad_norm(const double* partial, int n, float* norm, hipStream_t st) {
+  hipLaunchKernelGGL(grad_norm_kernel, dim3(1), dim3(1024), 0, st, partial, n, norm);
   return hipGetLastError();
 }
-hipError_t launch_grad_scale(const GradTable& t, int blocks, const double* factor, hipStream_t st) {
-  hipLaunchKernelGGL(grad_scale_kernel, dim3(blocks), dim3(kGradThreads), 0, st, t, factor);
+hipError_t launch_grad_scale(const GradTable& t, int blocks, const double* partial, int n, double max_norm, float* norm,
+                             hipStream_t st) {
+  if (t.count <= kGradShortTable)
+    hipLaunchKernelGGL(grad_scale_kernel<kGradShortTable>, dim3(blocks), dim3(kGradThreads), 0, st, short_table(t),
+                       partial, n, max_norm, norm);
+  else
+    hipLaunchKernelGGL(grad_scale_kernel<kGradTableSize>, dim3(blocks), dim3(kGradThreads), 0, st, t, partial, n,
+                       max_norm, norm);
   return hipGetLastError();
 }
 

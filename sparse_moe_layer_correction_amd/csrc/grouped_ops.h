@@ -78,21 +78,25 @@ hipError_t launch_fp8_blocks(const uint16_t* w, int64_t count, int N, int K, uin
 hipError_t launch_grouped_fp8(const Fp8Args& a, const GroupedPlan& plan, hipStream_t st);
 
 // Gradient tensors of one launch; entry i's chunks of kGradChunk elements are
-// first[i] .. first[i + 1] of the launch's (the last entry's end at chunks).
-constexpr int kGradTableSize = 120;
+// first[i] .. first[i + 1] of the launch's (the last entry's end at chunks). The
+// table is a kernel argument: few tensors take the short one.
+constexpr int kGradTableSize = 120, kGradShortTable = 16;
 constexpr int kGradChunk = 1 << 15;
-struct GradTable {
-  const void* src[kGradTableSize];
-  void* dst[kGradTableSize];
-  int64_t n[kGradTableSize];
-  int first[kGradTableSize];
-  uint32_t f32[(kGradTableSize + 31) / 32];   // bit i: entry i is fp32, else bf16
+template <int SIZE>
+struct GradTableOf {
+  const void* src[SIZE];
+  void* dst[SIZE];
+  int64_t n[SIZE];
+  int first[SIZE];
+  uint32_t f32[(SIZE + 31) / 32];   // bit i: entry i is fp32, else bf16
   int count, chunks;
 };
+typedef GradTableOf<kGradTableSize> GradTable;
 static_assert(sizeof(GradTable) <= 4000, "kernel arguments");
 hipError_t launch_grad_sumsq(const GradTable& t, int blocks, double* partial, hipStream_t st);
-hipError_t launch_grad_norm(const double* partial, int n, double max_norm, float* norm, double* factor,
-                            hipStream_t st);
-hipError_t launch_grad_scale(const GradTable& t, int blocks, const double* factor, hipStream_t st);
+hipError_t launch_grad_norm(const double* partial, int n, float* norm, hipStream_t st);
+// norm: where to write the norm (one launch of a call does), or null
+hipError_t launch_grad_scale(const GradTable& t, int blocks, const double* partial, int n, double max_norm, float* norm,
+                             hipStream_t st);
 
 }  // namespace moe

@@ -281,29 +281,35 @@ int check_tensors(const moe_grad_tensor* t, int32_t count) {
   return MOE_OK;
 }
 
-// Calls f(table, first tensor's index in order) for every launch's table of non-empty tensors.
+// Calls f(table) for every launch's table of non-empty tensors, in order or from the last tensor to the first.
 template <typename F>
-int for_tables(const moe_grad_tensor* t, int32_t count, F&& f) {
-  GradTable tab{};
+int for_tables(const moe_grad_tensor* t, int32_t count, bool reverse, F&& f) {
+  GradTable tab;
+  auto clear = [&]() {
+    tab.count = tab.chunks = 0;
+    for (uint32_t& w : tab.f32) w = 0;
+  };
+  clear();
   auto flush = [&]() -> int {
     if (tab.count == 0) return MOE_OK;
     const int rc = f(tab);
-    tab = GradTable{};
+    clear();
     return rc;
   };
-  for (int32_t i = 0; i < count; ++i) {
-    if (t[i].n == 0) continue;
-    const int64_t c = chunks_of(t[i].n);             // at most 2^25
+  for (int32_t j = 0; j < count; ++j) {
+    const moe_grad_tensor& g = t[reverse ? count - 1 - j : j];
+    if (g.n == 0) continue;
+    const int64_t c = chunks_of(g.n);                // at most 2^25
     if (tab.count == kGradTableSize || tab.chunks + c > 0x7FFFFFFF) {
       const int rc = flush();
       if (rc != MOE_OK) return rc;
     }
     const int k = tab.count++;
-    tab.src[k] = t[i].grad;
-    tab.dst[k] = t[i].out ? t[i].out : const_cast<void*>(t[i].grad);
-    tab.n[k] = t[i].n;
+    tab.src[k] = g.grad;
+    tab.dst[k] = g.out ? g.out : const_cast<void*>(g.grad);
+    tab.n[k] = g.n;
     tab.first[k] = tab.chunks;
-    if (t[i].dtype == MOE_FP32) tab.f32[k / 32] |= 1u << (k % 32);
+    if (g.dtype == MOE_FP32) tab.f32[k / 32] |= 1u << (k % 32);
     tab.chunks += (int)c;
   }
   return flush();
@@ -311,31 +317,47 @@ int for_tables(const moe_grad_tensor* t, int32_t count, F&& f) {
 
 int table_blocks(const GradTable& t) { return std::min(t.chunks, kGradBlocks); }
 
+// the partial sums' number: the workgroups of all launches
 size_t partials_of(const moe_grad_tensor* t, int32_t count) {
   size_t n = 0;
-  for_tables(t, count, [&](const GradTable& tab) -> int { n += table_blocks(tab); return MOE_OK; });
-  return n;
+  int in_table = 0;
+  int64_t chunks = 0;
+  for (int32_t i = 0; i < count; ++i) {
+    if (t[i].n == 0) continue;
+    const int64_t c = chunks_of(t[i].n);
+    if (in_table == kGradTableSize || chunks + c > 0x7FFFFFFF) {
+      n += (size_t)std::min<int64_t>(chunks, kGradBlocks);
+      in_table = 0;
+      chunks = 0;
+    }
+    ++in_table;
+    chunks += c;
+  }
+  return n + (size_t)std::min<int64_t>(chunks, kGradBlocks);
 }
+
+size_t grad_ws_bytes(size_t partials) { return align_up((partials + 1) * sizeof(double)); }
 
 int norm_impl(const moe_grad_tensor* t, int32_t count, double max_norm, float* norm, bool clip, void* ws,
               size_t ws_bytes, hipStream_t stream) {
   if (norm == nullptr) return MOE_ERR_INVALID;
   const size_t n = partials_of(t, count);
-  if (!ws_ok(ws, ws_bytes, align_up((n + 1) * 8))) return MOE_ERR_WORKSPACE;
-  double* factor = static_cast<double*>(ws);
-  double* partial = factor + 1;
+  if (!ws_ok(ws, ws_bytes, grad_ws_bytes(n))) return MOE_ERR_WORKSPACE;
+  double* partial = static_cast<double*>(ws);
   size_t at = 0;
-  int rc = for_tables(t, count, [&](const GradTable& tab) {
+  const int rc = for_tables(t, count, false, [&](const GradTable& tab) -> int {
     const int blocks = table_blocks(tab);
     const hipError_t e = launch_grad_sumsq(tab, blocks, partial + at, stream);
     at += blocks;
     return hip_status(e);
   });
   if (rc != MOE_OK) return rc;
-  rc = hip_status(launch_grad_norm(partial, (int)n, max_norm, norm, clip ? factor : nullptr, stream));
-  if (rc != MOE_OK || !clip) return rc;
-  return for_tables(t, count, [&](const GradTable& tab) {
-    return hip_status(launch_grad_scale(tab, table_blocks(tab), factor, stream));
+  if (!clip || n == 0) return hip_status(launch_grad_norm(partial, (int)n, norm, stream));
+  float* out = norm;
+  return for_tables(t, count, true, [&](const GradTable& tab) -> int {
+    const hipError_t e = launch_grad_scale(tab, table_blocks(tab), partial, (int)n, max_norm, out, stream);
+    out = nullptr;
+    return hip_status(e);
   });
 }
 
@@ -368,7 +390,7 @@ extern "C" {
 
 size_t moe_grad_norm_workspace_bytes(const moe_grad_tensor* tensors, int32_t count) {
   if (check_tensors(tensors, count) != MOE_OK) return 0;
-  return align_up((partials_of(tensors, count) + 1) * 8);
+  return grad_ws_bytes(partials_of(tensors, count));
 }
 
 int moe_grad_norm(const moe_grad_tensor* tensors, int32_t count, float* norm, void* ws, size_t ws_bytes,
