@@ -8,6 +8,10 @@ namespace moe {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
+// s_waitcnt vmcnt(n) lgkmcnt(0), and lgkmcnt(0) alone
+constexpr int wait_lgkm0(int n) { return (n & 0xF) | (0x7 << 4) | (((n >> 4) & 3) << 14); }
+constexpr int kWaitLgkm0 = 0xF | (0x7 << 4) | (3 << 14);
+
 // C tile BM x BN by WM x WN waves; k tiles of one block (128 codes, one line of
 // a row). The matrix instruction is 16x16x128: it sums a whole block into 4
 // registers per lane (row l & 15 of the rows' fragment, columns 4 (l >> 4) .. +
@@ -17,16 +21,27 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 //
 // A wave holds the block's TN weight fragments and streams its TM row
 // fragments: while fragment m is multiplied, m + 1 is read from LDS and the
-// sums of m - 1 are scaled and added. The one barrier of a k tile sits before
-// its last row fragment: past it the next tile has landed, nobody reads this
-// tile's stage, and the tile after the next is loaded there.
+// sums of m - 1 are scaled and added.
+//
+// What bounds it is the loads' latency (without them, on stale data, a k tile
+// took 1.29 us against 1.96): two stages of 64 KB fill the LDS, so each part of
+// a stage is loaded again as soon as it is free, not a whole stage at a time. A
+// k tile has two barriers. By the first, half way, its weight fragments (read
+// into registers before the tile began) and the first half of every wave's row
+// fragments are done with: those parts of the tile after the next are loaded.
+// Past the second, before the last row fragment, the second halves and the
+// scales follow, and the next tile's first fragments are read. Every load of
+// codes then has one and a half k tiles to land, and each barrier waits only
+// for what is read next.
 template <int BM, int BN, int WM, int WN, int OCC>
 __global__ void __launch_bounds__(64 * WM * WN, 1) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
 grouped_fp8_kernel(const Fp8Args P) {
   constexpr int NT = 64 * WM * WN;
   constexpr int WTN = BN / WN, TN = WTN / 16;
   static_assert(128 % WTN == 0, "a wave's columns lie in one weight block");
-  __shared__ u32x4 sa0[BM * 8], sb0[BN * 8], sa1[BM * 8], sb1[BN * 8];
+  // (the halves of the row stages are arrays of their own: the compiler waits for
+  // every load into an array before it reads from it)
+  __shared__ u32x4 sa0[BM * 4], sa0h[BM * 4], sb0[BN * 8], sa1[BM * 4], sa1h[BM * 4], sb1[BN * 8];
   __shared__ float sc0[BM], sc1[BM];
 
   const int tid = threadIdx.x, lane = tid & 63;
@@ -61,14 +76,21 @@ grouped_fp8_kernel(const Fp8Args P) {
   const int m0 = __builtin_amdgcn_readfirstlane(lo + mt * BM), n0 = __builtin_amdgcn_readfirstlane(nt * BN);
   const int K2 = P.K / 2;                              // the loads count pairs of codes
 
-  // HQ: the tile's height in quarters of BM (an expert's short last tile)
+  // HQ: the tile's height in quarters of BM (1, 2 or 4: an expert's last tile may be short)
   auto body = [&](auto height) __attribute__((always_inline)) {
     constexpr int HQ = decltype(height)::value;
     constexpr int H = BM * HQ / 4, WTM = H / WM, TM = WTM / 16;
-    static_assert(TM >= 1 && H * 8 % NT == 0, "wave tile");
-    OperandLoad<H, false, NT> la;
+    static_assert(TM >= 2 && TM % 2 == 0 && H * 8 % NT == 0, "wave tile");
+    // (a quarter tile's rows are one load a thread: they go whole, at the second barrier)
+    constexpr bool HALVES = HQ != 1;
+    constexpr int HR = HALVES ? H / 2 : H;            // rows of a row stage array
+    typedef OperandLoad<HR, false, NT, HALVES ? WTM / 2 : 0> LoadA;
+    constexpr int NA = LoadA::NL, NB = BN * 8 / NT;
+    LoadA la, lah;
     OperandLoad<BN, false, NT> lb;
-    la.init(reinterpret_cast<const uint16_t*>(P.A + (int64_t)m0 * P.K), K2, hi - m0, K2, wave, lane);
+    const uint16_t* rows8 = reinterpret_cast<const uint16_t*>(P.A + (int64_t)m0 * P.K);
+    la.init(rows8, K2, hi - m0, K2, wave, lane);
+    if constexpr (HALVES) lah.init(rows8, K2, hi - m0, K2, wave, lane, WTM / 2);
     lb.init(reinterpret_cast<const uint16_t*>(P.B + ((int64_t)e * P.N + n0) * P.K), K2, P.N - n0, K2, wave, lane);
 
     // a k tile's row scales: one dword per lane, 64 rows a wave (waves beyond
@@ -83,9 +105,10 @@ grouped_fp8_kernel(const Fp8Args P) {
                     live ? kRsrc2G : 0);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_ptr)&st[srow], 4, (int)sofs, 0, 0, 0);
     };
-    // the wave's weight scales, 64 blocks at a time in one register
-    const float* sw = P.sw + ((int64_t)e * P.nb + min((n0 + wave_n * WTN) / 128, P.nb - 1)) * P.kb;
-    float swv = sw[min(lane, P.kb - 1)];
+    // the wave's weight scales, one a k tile (scalar loads, through the constant address space)
+    typedef const __attribute__((address_space(4))) float* scale_ptr;
+    const scale_ptr sw = (scale_ptr)(uintptr_t)uniform_ptr(reinterpret_cast<const uint16_t*>(
+        P.sw + ((int64_t)e * P.nb + min((n0 + wave_n * WTN) / 128, P.nb - 1)) * P.kb));
 
     f32x4 acc[TM][TN];
 #pragma unroll
@@ -101,86 +124,99 @@ grouped_fp8_kernel(const Fp8Args P) {
     // constant offsets.
     const int r16 = lane & 15, swz = r16 >> 1, kc = 4 * (lane >> 5) + ((lane >> 4) & 1);
     const int c0 = r16 * 8 + (kc ^ swz), c1 = r16 * 8 + ((kc + 2) ^ swz);
-    const int a0 = wave_m * WTM * 8, b0 = wave_n * WTN * 8;
+    const int a0 = wave_m * (HALVES ? WTM / 2 : WTM) * 8, b0 = wave_n * WTN * 8;
     const int a_c0 = a0 + c0, a_c1 = a0 + c1, b_c0 = b0 + c0, b_c1 = b0 + c1;
     auto frag = [&](const u32x4* p0, const u32x4* p1, int row) {
       const u32x4 u = p0[row * 8], v = p1[row * 8];
       return i32x8{(int)u.x, (int)u.y, (int)u.z, (int)u.w, (int)v.x, (int)v.y, (int)v.z, (int)v.w};
     };
-    auto frag_a = [&](const u32x4* stage, int m) { return frag(stage + a_c0, stage + a_c1, m * 16); };
+    auto frag_a = [&](const u32x4* lo, const u32x4* hi, int m) {
+      const u32x4* p = HALVES && m >= TM / 2 ? hi : lo;
+      return frag(p + a_c0, p + a_c1, (HALVES && m >= TM / 2 ? m - TM / 2 : m) * 16);
+    };
     auto frag_b = [&](const u32x4* stage, int n) { return frag(stage + b_c0, stage + b_c1, n * 16); };
 
     i32x8 fb[TN], fa;
     f32x4 z[TN];                      // the sums of the row fragment before, not yet scaled
-    float zs = 0.f;
+    float w = sw[0];
+    float zs = 0.f, sv;               // their rows' scale times the weights'; the current fragment's row scale
 #pragma unroll
     for (int n = 0; n < TN; ++n) z[n] = f32x4{0.f, 0.f, 0.f, 0.f};
-    auto step = [&](int kt, u32x4* a, u32x4* b, float* sc, u32x4* a1, u32x4* b1) {
-      if (kt > 0 && (kt & 63) == 0) swv = sw[min(kt + lane, P.kb - 1)];
-      const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(swv), kt & 63));
-      float s[TM];
-#pragma unroll
-      for (int m = 0; m < TM; ++m) s[m] = sc[wave_m * WTM + m * 16 + r16] * w;
+    const int srow0 = wave_m * WTM + r16;
+    auto step = [&](int kt, u32x4* a, u32x4* ah, u32x4* b, float* sc, u32x4* a1, u32x4* b1, float* sc1) {
+      float wn;
 #pragma unroll
       for (int m = 0; m < TM; ++m) {
-        i32x8 fn, fbn[TN];
-        if (m + 1 < TM) {
-          fn = frag_a(a, m + 1);
-        } else {
-          asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        i32x8 fn;
+        float sn;
+        if (m == TM / 2) wn = sw[min(kt + 1, P.kb - 1)];
+        if (m + 1 == TM / 2) {
+          // (unsplit rows: the last barrier waited for the whole tile)
+          __builtin_amdgcn_s_waitcnt(HALVES ? wait_lgkm0(NB + 2 * NA + 1) : kWaitLgkm0);
+          asm volatile("s_barrier" ::: "memory");
           __builtin_amdgcn_sched_barrier(0);
-          la.issue(a, kt + 2, wave);
           lb.issue(b, kt + 2, wave);
-          issue_scales(sc, kt + 2);
-          fn = frag_a(a1, 0);
-#pragma unroll
-          for (int n = 0; n < TN; ++n) fbn[n] = frag_b(b1, n);
+          if constexpr (HALVES) la.issue(a, kt + 2, wave);
         }
-        f32x4 zn[TN];
-#pragma unroll
-        for (int n = 0; n < TN; ++n)
-          zn[n] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(fb[n], fa, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0,
-                                                                  0x7F7F7F7F, 0, 0x7F7F7F7F);
-        // (the first fragment adds the last one's of the tile before)
+        if (m + 1 < TM) {
+          fn = frag_a(a, ah, m + 1);
+          sn = sc[srow0 + (m + 1) * 16];
+        } else {
+          __builtin_amdgcn_s_waitcnt(wait_lgkm0(NB + (HALVES ? 2 * NA : 0)));
+          asm volatile("s_barrier" ::: "memory");
+          __builtin_amdgcn_sched_barrier(0);
+          issue_scales(sc, kt + 2);
+          if constexpr (HALVES) lah.issue(ah, kt + 2, wave);
+          else la.issue(a, kt + 2, wave);
+          fn = frag_a(a1, a1, 0);
+          sn = sc1[srow0];
+        }
+        // one matrix instruction, then the scaling of the sums it replaces (of the
+        // row fragment before; the tile's first fragment finishes the last one of
+        // the tile before). Pinned in this order: left to itself the compiler
+        // keeps more sums and fragments alive than there are registers.
         f32x4(&dst)[TN] = acc[m == 0 ? TM - 1 : m - 1];
 #pragma unroll
-        for (int n = 0; n < TN; ++n)
+        for (int n = 0; n < TN; ++n) {
+          const f32x4 zn = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+              fb[n], fa, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0x7F7F7F7F, 0, 0x7F7F7F7F);
+          if (m + 1 == TM) fb[n] = frag_b(b1, n);      // the next tile's, in the place of the one just used
 #pragma unroll
           for (int q = 0; q < 4; ++q) dst[n][q] = fmaf(z[n][q], zs, dst[n][q]);
-        // (pinned here: the compiler otherwise keeps every fragment's z until
-        // the end of the tile, and spills)
-#pragma unroll
-        for (int n = 0; n < TN; ++n) asm volatile("" : "+v"(dst[n]));
-#pragma unroll
-        for (int n = 0; n < TN; ++n) z[n] = zn[n];
-        zs = s[m];
-        fa = fn;
-        if (m + 1 == TM) {
-#pragma unroll
-          for (int n = 0; n < TN; ++n) fb[n] = fbn[n];
+          asm volatile("" : "+v"(dst[n]));
+          z[n] = zn;
+          __builtin_amdgcn_sched_barrier(0);
         }
-        __builtin_amdgcn_sched_barrier(0);   // (left to itself the scheduler reads every fragment first, and spills)
+        zs = sv * w;
+        sv = sn;
+        if (m + 1 == TM) w = wn;
+        fa = fn;
       }
     };
-    constexpr int NL = OperandLoad<H, false, NT>::NL + OperandLoad<BN, false, NT>::NL + 1;
-    la.issue(sa0, 0, wave);
-    lb.issue(sb0, 0, wave);
-    issue_scales(sc0, 0);
-    la.issue(sa1, 1, wave);
-    lb.issue(sb1, 1, wave);
-    issue_scales(sc1, 1);
-    MOE_WAIT_VMCNT(NL);
+    // in the order of the steps: what the second barrier of the step before waits
+    // for, then what later ones do
+    auto start = [&](int kt, u32x4* a, u32x4* ah, u32x4* b, float* sc) {
+      lb.issue(b, kt, wave);
+      if constexpr (HALVES) la.issue(a, kt, wave);
+      issue_scales(sc, kt);
+      if constexpr (HALVES) lah.issue(ah, kt, wave);
+      else la.issue(a, kt, wave);
+    };
+    start(0, sa0, sa0h, sb0, sc0);
+    start(1, sa1, sa1h, sb1, sc1);
+    MOE_WAIT_VMCNT(NB + 1 + (HALVES ? 3 * NA : NA));
     asm volatile("s_barrier" ::: "memory");
     __builtin_amdgcn_sched_barrier(0);
-    fa = frag_a(sa0, 0);
+    fa = frag_a(sa0, sa0, 0);
+    sv = sc0[srow0];
 #pragma unroll
     for (int n = 0; n < TN; ++n) fb[n] = frag_b(sb0, n);
     int kt = 0;
     for (; kt + 1 < P.kb; kt += 2) {
-      step(kt, sa0, sb0, sc0, sa1, sb1);
-      step(kt + 1, sa1, sb1, sc1, sa0, sb0);
+      step(kt, sa0, sa0h, sb0, sc0, sa1, sb1, sc1);
+      step(kt + 1, sa1, sa1h, sb1, sc1, sa0, sb0, sc0);
     }
-    if (kt < P.kb) step(kt, sa0, sb0, sc0, sa1, sb1);
+    if (kt < P.kb) step(kt, sa0, sa0h, sb0, sc0, sa1, sb1, sc1);
 #pragma unroll
     for (int n = 0; n < TN; ++n)
 #pragma unroll
@@ -189,10 +225,17 @@ grouped_fp8_kernel(const Fp8Args P) {
     __syncthreads();
 
     // through LDS to whole rows of the wave tile, as store_wave_tile
-    constexpr int per = BM * 8 * 16 / 16384, CPW = WTN / 8, RPI = 64 / CPW, NRB = WTM / RPI;
-    static_assert(WM * WN <= 4 * per && WTM * WTN * 2 <= 16384, "staging areas");
-    const int h = wave / per;
-    char* stg = reinterpret_cast<char*>(h == 0 ? sa0 : h == 1 ? sb0 : h == 2 ? sa1 : sb1) + (wave % per) * 16384;
+    constexpr int CPW = WTN / 8, RPI = 64 / CPW, NRB = WTM / RPI, SB = WTM * WTN * 2;
+    constexpr int APER = BM * 64 / SB, BPER = BN * 128 / SB;     // wave tiles in a row half, in a weight stage
+    static_assert(APER >= 1 && WM * WN <= 4 * APER + 2 * BPER, "staging areas");
+    u32x4* const area = wave < BPER                 ? sb0
+                        : wave < 2 * BPER            ? sb1
+                        : wave < 2 * BPER + APER     ? sa0
+                        : wave < 2 * BPER + 2 * APER ? sa0h
+                        : wave < 2 * BPER + 3 * APER ? sa1
+                                                     : sa1h;
+    char* stg = reinterpret_cast<char*>(area) +
+                (wave < 2 * BPER ? wave % BPER : (wave - 2 * BPER) % APER) * SB;
 #pragma unroll
     for (int m = 0; m < TM; ++m) {
       const int r = m * 16 + r16;
@@ -222,7 +265,6 @@ grouped_fp8_kernel(const Fp8Args P) {
     const int rows = hi - m0;
     if (rows <= 64) { body(Stage<1>{}); return; }
     if (rows <= 128) { body(Stage<2>{}); return; }
-    if (rows <= 192) { body(Stage<3>{}); return; }
   }
   body(Stage<4>{});
 }

@@ -157,30 +157,42 @@ __device__ __forceinline__ int swz_tr(int k, int c) {
 
 // Loads of one operand's [64-deep k tile] stage: W tile rows (columns of C or
 // rows of C), TR: stored reduction-major.
-template <int W, bool TR, int NT>
+// HS (not TR): not 0, the stage holds half of the tile: of every strip of 2 HS
+// rows the HS rows from `half` on.
+template <int W, bool TR, int NT, int HS = 0>
 struct OperandLoad {
   static constexpr int NL = W * 8 / NT;      // 16-byte loads per thread
+  static_assert(HS == 0 || (!TR && HS % 8 == 0), "halves");
   const uint16_t* base;                      // tile's first element (not TR), or first column (TR)
   int64_t ld;
   int klen;
   uint32_t ofs[NL];
-  int kc[NL];                                // not TR: first k of the lane's chunk inside the tile
+  uint64_t tail0, tail1;                     // not TR: the lanes whose chunk lies inside the last k tile,
+                                             //   for the loads of even and of odd 8-row blocks
+  // load i of a wave fills the 64 chunks (8 rows) from here on
+  static __device__ __forceinline__ int chunk(int wave, int i) { return (wave * NL + i) * 64; }
   // width: valid tile rows
-  __device__ __forceinline__ void init(const uint16_t* p, int64_t ld_, int width, int klen_, int wave, int lane) {
+  __device__ __forceinline__ void init(const uint16_t* p, int64_t ld_, int width, int klen_, int wave, int lane,
+                                       int half = 0) {
     base = p;
     ld = ld_;
     klen = klen_;
+    if constexpr (!TR) {
+      const int left = klen - (klen - 1) / 64 * 64;
+      tail0 = __ballot(swz_slot(lane / 8, lane % 8) * 8 < left);
+      tail1 = __ballot(swz_slot(8 + lane / 8, lane % 8) * 8 < left);
+    }
 #pragma unroll
     for (int i = 0; i < NL; ++i) {
-      const int q = (wave * NL + i) * 64 + lane;
+      const int q = chunk(wave, i) + lane;
       if constexpr (TR) {
         const int k = q / (W / 8), c = swz_tr<W>(k, q % (W / 8));
         ofs[i] = c * 8 < width ? (uint32_t)(k * ld * 2 + c * 16) : kOutOfRange;
-        kc[i] = 0;
       } else {
-        const int r = q / 8, c = swz_slot(r, q % 8);
+        int r = q / 8;
+        const int c = swz_slot(r, q % 8);
+        if constexpr (HS > 0) r = r / HS * (2 * HS) + half + r % HS;
         ofs[i] = r < width ? (uint32_t)(r * ld * 2 + c * 16) : kOutOfRange;
-        kc[i] = c * 8;
       }
     }
   }
@@ -192,15 +204,19 @@ struct OperandLoad {
                                                  __builtin_amdgcn_readfirstlane((int)(rows * ld * 2)));
 #pragma unroll
       for (int i = 0; i < NL; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_ptr)&stage[(wave * NL + i) * 64], 16, (int)ofs[i], 0, 0,
-                                                 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_ptr)&stage[chunk(wave, i)], 16, (int)ofs[i], 0, 0, 0);
     } else {
       const __amdgpu_buffer_rsrc_t r = make_rsrc(base, left > 0 ? kRsrc2G : 0);
       const int so = left > 0 ? kt * 128 : 0;
+      const bool whole = left >= 64;
 #pragma unroll
       for (int i = 0; i < NL; ++i)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_ptr)&stage[(wave * NL + i) * 64], 16,
-                                                 (int)(kc[i] < left ? ofs[i] : kOutOfRange), so, 0, 0);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_ptr)&stage[chunk(wave, i)], 16,
+                                                 (int)(__builtin_amdgcn_inverse_ballot_w64(
+                                                           whole ? ~0ull : (chunk(wave, i) >> 6) & 1 ? tail1 : tail0)
+                                                           ? ofs[i]
+                                                           : kOutOfRange),
+                                                 so, 0, 0);
     }
   }
 };
