@@ -182,9 +182,15 @@ def _check(rc: int):
 # tensor plumbing
 # ----------------------------------------------------------------------------
 
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _ptr(t) -> Optional[int]:
@@ -546,38 +552,33 @@ def bias_update(offsets, corr_bias, eta: float, *, stream=None):
 # the experts' products on their own, their gradients, 8-bit experts
 # ----------------------------------------------------------------------------
 
-def _elsewhere(device, stream):
-    """None if a call on tensors of ``device`` can go straight to the current stream; else the
-    context to make it in (``stream`` current, or the tensors' device), so that what it
-    allocates is reused in that stream's order."""
+def _elsewhere(t, stream):
+    """None if a call on tensor ``t`` can go straight to the current stream; else the context to
+    make it in (``stream`` current, or the tensor's device), so that what it allocates is
+    reused in that stream's order."""
     torch = _torch()
-    if device.type != "cuda":
-        raise ValueError(f"tensors must be on the GPU, got {device}")
+    index = t.get_device()
+    if index < 0:
+        raise ValueError(f"tensors must be on the GPU, got {t.device}")
     if stream is not None:
-        if stream.device != device:
-            raise ValueError(f"stream belongs to {stream.device}, the tensors to {device}")
+        if stream.device != t.device:
+            raise ValueError(f"stream belongs to {stream.device}, the tensors to {t.device}")
         return torch.cuda.stream(stream)
-    return None if torch.cuda.current_device() == device.index else torch.cuda.device(device)
+    return None if torch.cuda.current_device() == index else torch.cuda.device(index)
 
 
-def _raw_stream(device) -> int:
-    # (torch.cuda.current_stream wraps the same handle in a Stream object: 2 us a call)
-    return _torch()._C._cuda_getCurrentRawStream(device.index)
-
-
-def _need_rows(t, name, dtype, rows, cols, device):
-    """A matrix [rows, cols] whose columns are contiguous; returns its row stride."""
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
+def _need_rows(t, name, dtype, rows, cols, index):
+    """A matrix [rows, cols] on GPU `index` whose columns are contiguous; returns its row stride."""
+    if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name} must be a torch tensor")
-    if t.dtype != dtype:
+    if t.dtype is not dtype:
         raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.shape != (rows, cols):
         raise ValueError(f"{name} must have shape {(rows, cols)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on the GPU device {device}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on GPU {index}, got {t.device}")
     rs, cs = t.stride()
-    if cols > 1 and cs != 1 and rows:
+    if cs != 1 and cols > 1 and rows:
         raise ValueError(f"{name}'s columns must be contiguous, got strides {(rs, cs)}")
     if rows <= 1:
         return cols
@@ -586,20 +587,22 @@ def _need_rows(t, name, dtype, rows, cols, device):
     return rs
 
 
-def _need_weight(w, offsets, dtype, device):
-    """w [E, N, K] and offsets [E+1]; returns E, N, K, the row and the expert stride."""
+def _need_weight(w, offsets, dtype, index):
+    """w [E, N, K] and offsets [E+1] on GPU `index`; returns E, N, K, the row and the expert stride."""
     torch = _torch()
     if not isinstance(w, torch.Tensor) or not isinstance(offsets, torch.Tensor):
         raise TypeError("w and offsets must be torch tensors")
     if w.dim() != 3:
         raise ValueError(f"w must have 3 dimensions, got shape {tuple(w.shape)}")
     E, N, K = w.shape
-    if w.dtype != dtype or offsets.dtype != torch.int32:
+    if w.dtype is not dtype or offsets.dtype is not torch.int32:
         raise TypeError(f"w must be {dtype} and offsets int32, got {w.dtype} and {offsets.dtype}")
-    if w.device != device or offsets.device != device:
-        raise ValueError(f"w and offsets must be on the GPU device {device}")
-    if offsets.shape != (E + 1,) or (E and offsets.stride(0) != 1):
+    if w.get_device() != index or offsets.get_device() != index:
+        raise ValueError(f"w and offsets must be on GPU {index}, got {w.device} and {offsets.device}")
+    if offsets.dim() != 1 or offsets.numel() != E + 1 or not offsets.is_contiguous():
         raise ValueError(f"offsets must be contiguous of shape {(E + 1,)}, got {tuple(offsets.shape)}")
+    if w.is_contiguous():
+        return E, N, K, K, N * K
     es, ldw, ks = w.stride()
     if N <= 1:
         ldw = K
@@ -611,8 +614,7 @@ def _need_weight(w, offsets, dtype, device):
 
 
 def _need_matrix(t, name):
-    torch = _torch()
-    if not isinstance(t, torch.Tensor):
+    if not isinstance(t, _torch().Tensor):
         raise TypeError(f"{name} must be a torch tensor")
     if t.dim() != 2:
         raise ValueError(f"{name} must have 2 dimensions, got shape {tuple(t.shape)}")
@@ -621,21 +623,23 @@ def _need_matrix(t, name):
 _ERR_WORKSPACE = -3
 
 
-def _grouped_call(fn, d: _GroupedDims, device, ws, *args):
-    """fn(d, *args, ws, ws_bytes, stream) on the current stream. Without a caller's workspace
-    the first try has none, which small calls do not need; the others refuse before any
-    launch and get one."""
+def _grouped_call(fn, d: _GroupedDims, index, ws, *args):
+    """fn(d, *args, ws, ws_bytes, stream) on GPU `index`'s current stream. Without a caller's
+    workspace the first try has none, which small calls do not need; the others refuse
+    before any launch and get one."""
+    torch = _torch()
     dr = ctypes.byref(d)
-    stream = _raw_stream(device)
+    # (torch.cuda.current_stream wraps the same handle in a Stream object: 2 us a call)
+    stream = torch._C._cuda_getCurrentRawStream(index)
     if ws is None:
         rc = fn(dr, *args, None, 0, stream)
         if rc == _ERR_WORKSPACE:
             nbytes = load_library().moe_grouped_workspace_bytes(dr)
-            ws = _torch().empty(nbytes, dtype=_torch().uint8, device=device)
+            ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
             rc = fn(dr, *args, ws.data_ptr(), nbytes, stream)
     else:
-        if ws.device != device:
-            raise ValueError(f"ws must be on the GPU device {device}")
+        if ws.get_device() != index:
+            raise ValueError(f"ws must be on GPU {index}, got {ws.device}")
         rc = fn(dr, *args, ws.data_ptr(), ws.numel() * ws.element_size(), stream)
     if rc != 0:
         _check(rc)
@@ -654,23 +658,23 @@ def grouped_matmul(x, w, offsets, *, out=None, ws=None, stream=None):
     belong to no expert are left as they are in ``out`` (zero when it is not given)."""
     torch = _torch()
     _need_matrix(x, "x")
-    dev = x.device
-    ctx = _elsewhere(dev, stream)
+    ctx = _elsewhere(x, stream)
     if ctx is not None:
         with ctx:
             return grouped_matmul(x, w, offsets, out=out, ws=ws)
-    E, N, K, ldw, es = _need_weight(w, offsets, torch.bfloat16, dev)
+    index = x.get_device()
+    E, N, K, ldw, es = _need_weight(w, offsets, torch.bfloat16, index)
     R = x.shape[0]
-    ldx = _need_rows(x, "x", torch.bfloat16, R, K, dev)
+    ldx = _need_rows(x, "x", torch.bfloat16, R, K, index)
     fresh = out is None
     if fresh:
-        out = torch.empty(R, N, dtype=torch.bfloat16, device=dev)
+        out = torch.empty(R, N, dtype=torch.bfloat16, device=x.device)
         ldy = N
     else:
-        ldy = _need_rows(out, "out", torch.bfloat16, R, N, dev)
+        ldy = _need_rows(out, "out", torch.bfloat16, R, N, index)
     lib = load_library()
     d = _GroupedDims(R, E, N, K, ldx, ldy, ldw, es, 0, fresh)
-    _grouped_call(lib.moe_grouped_matmul, d, dev, ws, x.data_ptr(), w.data_ptr(), offsets.data_ptr(), out.data_ptr())
+    _grouped_call(lib.moe_grouped_matmul, d, index, ws, x.data_ptr(), w.data_ptr(), offsets.data_ptr(), out.data_ptr())
     return out
 
 
@@ -684,16 +688,16 @@ def grouped_matmul_grad(dy, x, w, offsets, *, need_dx: bool = True, need_dw: boo
     torch = _torch()
     _need_matrix(x, "x")
     _need_matrix(dy, "dy")
-    dev = x.device
-    ctx = _elsewhere(dev, stream)
+    ctx = _elsewhere(x, stream)
     if ctx is not None:
         with ctx:
             return grouped_matmul_grad(dy, x, w, offsets, need_dx=need_dx, need_dw=need_dw, dx=dx, dw=dw,
                                        dw_dtype=dw_dtype, accumulate=accumulate, ws=ws)
-    E, N, K, ldw, es = _need_weight(w, offsets, torch.bfloat16, dev)
+    index = x.get_device()
+    E, N, K, ldw, es = _need_weight(w, offsets, torch.bfloat16, index)
     R = x.shape[0]
-    ldx = _need_rows(x, "x", torch.bfloat16, R, K, dev)
-    ldy = _need_rows(dy, "dy", torch.bfloat16, R, N, dev)
+    ldx = _need_rows(x, "x", torch.bfloat16, R, K, index)
+    ldy = _need_rows(dy, "dy", torch.bfloat16, R, N, index)
     if not (need_dx or need_dw):
         raise ValueError("one of need_dx and need_dw must be set")
     if accumulate and (dw is None or not need_dw):
@@ -706,18 +710,18 @@ def grouped_matmul_grad(dy, x, w, offsets, *, need_dx: bool = True, need_dw: boo
     if not need_dx:
         dx = None
     elif fresh:
-        dx = torch.empty(R, K, dtype=torch.bfloat16, device=dev)
+        dx = torch.empty(R, K, dtype=torch.bfloat16, device=x.device)
     else:
-        lddx = _need_rows(dx, "dx", torch.bfloat16, R, K, dev)
+        lddx = _need_rows(dx, "dx", torch.bfloat16, R, K, index)
     if not need_dw:
         dw = None
     elif dw is None:
-        dw = torch.empty(E, N, K, dtype=dw_dtype, device=dev)
+        dw = torch.empty(E, N, K, dtype=dw_dtype, device=x.device)
     else:
-        _need(dw, "dw", dw_dtype, (E, N, K), dev)
+        _need(dw, "dw", dw_dtype, (E, N, K), x.device)
     lib = load_library()
     d = _GroupedDims(R, E, N, K, ldx, ldy, ldw, es, lddx, fresh)
-    _grouped_call(lib.moe_grouped_matmul_grad, d, dev, ws, dy.data_ptr(), x.data_ptr(), w.data_ptr(),
+    _grouped_call(lib.moe_grouped_matmul_grad, d, index, ws, dy.data_ptr(), x.data_ptr(), w.data_ptr(),
                   offsets.data_ptr(), _ptr(dx), _ptr(dw), dw_dtype == torch.float32, accumulate)
     return dx, dw
 
@@ -726,17 +730,17 @@ def quantize_fp8_rows(x, *, stream=None):
     """moe_quantize_fp8_rows: x [R, K] bf16 -> (codes uint8 [R, K], scales fp32 [ceil(K/128), R])."""
     torch = _torch()
     _need_matrix(x, "x")
-    dev = x.device
-    ctx = _elsewhere(dev, stream)
+    ctx = _elsewhere(x, stream)
     if ctx is not None:
         with ctx:
             return quantize_fp8_rows(x)
     R, K = x.shape
-    ldx = _need_rows(x, "x", torch.bfloat16, R, K, dev)
-    codes = torch.empty(R, K, dtype=torch.uint8, device=dev)
-    scales = torch.empty((K + 127) // 128, R, dtype=torch.float32, device=dev)
+    index = x.get_device()
+    ldx = _need_rows(x, "x", torch.bfloat16, R, K, index)
+    codes = torch.empty(R, K, dtype=torch.uint8, device=x.device)
+    scales = torch.empty((K + 127) // 128, R, dtype=torch.float32, device=x.device)
     _check(load_library().moe_quantize_fp8_rows(x.data_ptr(), R, K, ldx, codes.data_ptr(), scales.data_ptr(),
-                                                _raw_stream(dev)))
+                                                torch._C._cuda_getCurrentRawStream(index)))
     return codes, scales
 
 
@@ -746,18 +750,17 @@ def quantize_fp8_blocks(w, *, stream=None):
     torch = _torch()
     if not isinstance(w, torch.Tensor) or w.dim() < 2 or w.dtype != torch.bfloat16:
         raise TypeError("w must be a [..., N, K] bf16 torch tensor")
-    dev = w.device
-    ctx = _elsewhere(dev, stream)
+    ctx = _elsewhere(w, stream)
     if ctx is not None:
         with ctx:
             return quantize_fp8_blocks(w)
-    _need(w, "w", torch.bfloat16, w.shape, dev)
+    _need(w, "w", torch.bfloat16, w.shape, w.device)
     N, K = w.shape[-2:]
     count = w.numel() // (N * K) if N * K else 0
-    codes = torch.empty(w.shape, dtype=torch.uint8, device=dev)
-    scales = torch.empty(w.shape[:-2] + ((N + 127) // 128, (K + 127) // 128), dtype=torch.float32, device=dev)
+    codes = torch.empty(w.shape, dtype=torch.uint8, device=w.device)
+    scales = torch.empty(w.shape[:-2] + ((N + 127) // 128, (K + 127) // 128), dtype=torch.float32, device=w.device)
     _check(load_library().moe_quantize_fp8_blocks(w.data_ptr(), count, N, K, codes.data_ptr(), scales.data_ptr(),
-                                                  _raw_stream(dev)))
+                                                  torch._C._cuda_getCurrentRawStream(w.get_device())))
     return codes, scales
 
 
@@ -770,12 +773,12 @@ def grouped_matmul_fp8(x, w_codes, w_scale, offsets, *, x_scale=None, out=None, 
     ``grouped_matmul``)."""
     torch = _torch()
     _need_matrix(x, "x")
-    dev = x.device
-    ctx = _elsewhere(dev, stream)
+    ctx = _elsewhere(x, stream)
     if ctx is not None:
         with ctx:
             return grouped_matmul_fp8(x, w_codes, w_scale, offsets, x_scale=x_scale, out=out, ws=ws)
-    E, N, K, ldw, es = _need_weight(w_codes, offsets, torch.uint8, dev)
+    index, dev = x.get_device(), x.device
+    E, N, K, ldw, es = _need_weight(w_codes, offsets, torch.uint8, index)
     R = x.shape[0]
     kb, nb = (K + 127) // 128, (N + 127) // 128
     if not w_codes.is_contiguous():
@@ -783,23 +786,23 @@ def grouped_matmul_fp8(x, w_codes, w_scale, offsets, *, x_scale=None, out=None, 
     _need(w_scale, "w_scale", torch.float32, (E, nb, kb), dev)
     ldx = 0
     if x_scale is None:
-        ldx = _need_rows(x, "x", torch.bfloat16, R, K, dev)
+        ldx = _need_rows(x, "x", torch.bfloat16, R, K, index)
     else:
         _need(x, "x", torch.uint8, (R, K), dev)
         _need(x_scale, "x_scale", torch.float32, (kb, R), dev)
     fresh = out is None
     if fresh:
-        out = torch.empty(R, N, dtype=torch.bfloat16, device=dev)
+        out = torch.empty(R, N, dtype=torch.bfloat16, device=x.device)
         ldy = N
     else:
-        ldy = _need_rows(out, "out", torch.bfloat16, R, N, dev)
+        ldy = _need_rows(out, "out", torch.bfloat16, R, N, index)
     lib = load_library()
     d = _GroupedDims(R, E, N, K, ldx, ldy, 0, 0, 0, fresh)
     if x_scale is None:
-        _grouped_call(lib.moe_grouped_matmul_fp8_rows, d, dev, ws, x.data_ptr(), w_codes.data_ptr(),
+        _grouped_call(lib.moe_grouped_matmul_fp8_rows, d, index, ws, x.data_ptr(), w_codes.data_ptr(),
                       w_scale.data_ptr(), offsets.data_ptr(), out.data_ptr())
     else:
-        _grouped_call(lib.moe_grouped_matmul_fp8, d, dev, ws, x.data_ptr(), x_scale.data_ptr(), w_codes.data_ptr(),
+        _grouped_call(lib.moe_grouped_matmul_fp8, d, index, ws, x.data_ptr(), x_scale.data_ptr(), w_codes.data_ptr(),
                       w_scale.data_ptr(), offsets.data_ptr(), out.data_ptr())
     return out
 
@@ -809,7 +812,7 @@ def grouped_matmul_fp8(x, w_codes, w_scale, offsets, *, x_scale=None, out=None, 
 # ----------------------------------------------------------------------------
 
 def _grad_table(grads, out):
-    """The moe_grad_tensor array of ``grads`` (and their number and device)."""
+    """The moe_grad_tensor array of ``grads`` (as a pointer and its storage), their number, the first tensor."""
     torch = _torch()
     grads = list(grads)
     outs = grads if out is None else list(out)
@@ -840,16 +843,20 @@ def _grad_table(grads, out):
             at = o.data_ptr()
         words += (g.data_ptr(), at, n, 0 if dt is bf16 else 1)
     raw = (ctypes.c_int64 * len(words))(*words)
-    return ctypes.cast(raw, ctypes.POINTER(_GradTensor)), raw, len(grads), grads[0].device
+    return ctypes.cast(raw, ctypes.POINTER(_GradTensor)), raw, len(grads), grads[0]
 
 
-def _grad_ws(lib, tab, n, device, ws):
-    if ws is not None:
-        if ws.device != device:
-            raise ValueError(f"ws must be on the GPU device {device}")
-        return ws, ws.numel() * ws.element_size()
-    nbytes = lib.moe_grad_norm_workspace_bytes(tab, n)
-    return _torch().empty(max(nbytes, 1), dtype=_torch().uint8, device=device), nbytes
+def _grad_call(fn, tab, n, index, ws, *args):
+    torch = _torch()
+    stream = torch._C._cuda_getCurrentRawStream(index)
+    if ws is None:
+        nbytes = load_library().moe_grad_norm_workspace_bytes(tab, n)
+        ws = torch.empty(max(nbytes, 1), dtype=torch.uint8, device=torch.device("cuda", index))
+    else:
+        if ws.get_device() != index:
+            raise ValueError(f"ws must be on GPU {index}, got {ws.device}")
+        nbytes = ws.numel() * ws.element_size()
+    _check(fn(tab, n, *args, ws.data_ptr(), nbytes, stream))
 
 
 def grad_norm(grads, *, ws=None, stream=None):
@@ -857,15 +864,13 @@ def grad_norm(grads, *, ws=None, stream=None):
     GPU, contiguous) as a 0-dimensional fp32 tensor on that GPU."""
     torch = _torch()
     grads = list(grads)
-    tab, _keep, n, dev = _grad_table(grads, None)
-    ctx = _elsewhere(dev, stream)
+    tab, _keep, n, first = _grad_table(grads, None)
+    ctx = _elsewhere(first, stream)
     if ctx is not None:
         with ctx:
             return grad_norm(grads, ws=ws)
-    lib = load_library()
-    norm = torch.empty((), dtype=torch.float32, device=dev)
-    ws, nbytes = _grad_ws(lib, tab, n, dev, ws)
-    _check(lib.moe_grad_norm(tab, n, norm.data_ptr(), ws.data_ptr(), nbytes, _raw_stream(dev)))
+    norm = torch.empty((), dtype=torch.float32, device=first.device)
+    _grad_call(load_library().moe_grad_norm, tab, n, first.get_device(), ws, norm.data_ptr())
     return norm
 
 
@@ -876,15 +881,13 @@ def clip_grad_norm(grads, max_norm: float, *, out=None, ws=None, stream=None):
     torch = _torch()
     grads = list(grads)
     out = None if out is None else list(out)
-    tab, _keep, n, dev = _grad_table(grads, out)
-    ctx = _elsewhere(dev, stream)
+    tab, _keep, n, first = _grad_table(grads, out)
+    ctx = _elsewhere(first, stream)
     if ctx is not None:
         with ctx:
             return clip_grad_norm(grads, max_norm, out=out, ws=ws)
-    lib = load_library()
-    norm = torch.empty((), dtype=torch.float32, device=dev)
-    ws, nbytes = _grad_ws(lib, tab, n, dev, ws)
-    _check(lib.moe_clip_grad_norm(tab, n, max_norm, norm.data_ptr(), ws.data_ptr(), nbytes, _raw_stream(dev)))
+    norm = torch.empty((), dtype=torch.float32, device=first.device)
+    _grad_call(load_library().moe_clip_grad_norm, tab, n, first.get_device(), ws, max_norm, norm.data_ptr())
     return norm
 
 

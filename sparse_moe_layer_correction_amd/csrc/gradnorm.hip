@@ -61,8 +61,8 @@ __global__ void __launch_bounds__(kGradThreads) grad_sumsq_kernel(const GradTabl
   double s = 0.0;
   for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
     const int i = grad_entry(t, c);
-    const int64_t at = (int64_t)(c - t.first[i]) * kGradChunk;
-    const int n = (int)min((int64_t)kGradChunk, t.n[i] - at);
+    const int64_t at = (int64_t)(c - t.first[i]) << t.chunk_log2;
+    const int n = (int)min((int64_t)1 << t.chunk_log2, t.n[i] - at);
     if ((t.f32[i >> 5] >> (i & 31)) & 1) {
       const float* p = static_cast<const float*>(t.src[i]) + at;
       const int h = head_of(p, n), nv = (n - h) / 4, tail = h + nv * 4;
@@ -119,8 +119,8 @@ __global__ void __launch_bounds__(kGradThreads) grad_scale_kernel(const GradTabl
   for (int c = t.chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
     const int i = grad_entry(t, c);
     if (f == 1.0 && t.src[i] == t.dst[i]) continue;      // in place and nothing to scale
-    const int64_t at = (int64_t)(c - t.first[i]) * kGradChunk;
-    const int n = (int)min((int64_t)kGradChunk, t.n[i] - at);
+    const int64_t at = (int64_t)(c - t.first[i]) << t.chunk_log2;
+    const int n = (int)min((int64_t)1 << t.chunk_log2, t.n[i] - at);
     if ((t.f32[i >> 5] >> (i & 31)) & 1) {
       const float* p = static_cast<const float*>(t.src[i]) + at;
       float* o = static_cast<float*>(t.dst[i]) + at;
@@ -163,6 +163,7 @@ static GradTableOf<kGradShortTable> short_table(const GradTable& t) {
   s.f32[0] = t.f32[0];
   s.count = t.count;
   s.chunks = t.chunks;
+  s.chunk_log2 = t.chunk_log2;
   return s;
 }
 

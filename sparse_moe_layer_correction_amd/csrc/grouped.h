@@ -44,77 +44,62 @@ struct GroupedArgs {
                                //   fp32 sums go to C + i * c_estride
 };
 
-// Finds, in one wave and from the offsets alone, what the tile table holds: lane
-// l takes the C = ceil(E / 64) experts from l * C on. About 1.5 us for a
-// workgroup, against a launch of its own for the table: taken for the grids of
-// few workgroups (grouped.hip).
+// Finds, in one wave and from the offsets alone, what the tile table holds, for
+// up to 128 experts: lane l has the experts 2 l and 2 l + 1. One round of loads
+// and two scans over the lanes, against a launch of its own for the table: taken
+// for the grids of few workgroups (grouped.hip).
+constexpr int kScanExperts = 2 * kWave;
 struct OffsetScan {
-  const int32_t* off;
-  int E, R, C, e0;
-  int base;            // the running maximum before the lane's experts
-  __device__ __forceinline__ int at(int i) const { return min(max(off[min(i, E)], 0), R); }
-  __device__ __forceinline__ OffsetScan(const int32_t* offsets, int E_, int R_, int lane) : off(offsets), E(E_), R(R_) {
-    C = (E + kWave - 1) / kWave;
-    e0 = lane * C;
-    int v = 0;
-    for (int j = 0; j < C; ++j) v = max(v, at(e0 + j));
+  int E, e0;
+  int lo, mid, hi;     // the lane's experts have the rows [lo, mid) and [mid, hi); none past E
+  __device__ __forceinline__ OffsetScan(const int32_t* offsets, int E_, int R, int lane) : E(E_), e0(2 * lane) {
+    auto at = [&](int i) { return min(max(offsets[min(i, E_)], 0), R); };
+    lo = at(e0);
+    mid = max(lo, at(e0 + 1));
+    hi = at(e0 + 2);
+    int v = mid;                                     // the running maximum up to the lane's second start
 #pragma unroll
     for (int d = 1; d < kWave; d <<= 1) {
       const int o = __shfl_up(v, d, kWave);
       if (lane >= d) v = max(v, o);
     }
     const int before = __shfl_up(v, 1, kWave);
-    base = lane == 0 ? 0 : before;
-  }
-  // f(e, lo, hi) for the lane's experts in order
-  template <typename F>
-  __device__ __forceinline__ void each(F&& f) const {
-    int v = base;
-    for (int j = 0; j < C && e0 + j < E; ++j) {
-      const int lo = max(v, at(e0 + j)), hi = max(lo, at(e0 + j + 1));
-      f(e0 + j, lo, hi);
-      v = lo;
-    }
+    if (lane > 0) lo = max(lo, before);
+    mid = v;
+    hi = max(hi, mid);
+    if (e0 >= E) mid = hi = lo;                      // (past the end every offset read is the last one)
+    else if (e0 + 1 >= E) hi = mid;
   }
   // rows of expert e, the same in every lane
   __device__ __forceinline__ int2 rows(int e) const {
-    int lo = 0, hi = 0;
-    each([&](int i, int a, int b) {
-      if (i == e) { lo = a; hi = b; }
-    });
-    const int src = e / C;
-    return make_int2(__builtin_amdgcn_readlane(lo, src), __builtin_amdgcn_readlane(hi, src));
+    const int a = e & 1 ? mid : lo, b = e & 1 ? hi : mid;
+    return make_int2(__builtin_amdgcn_readlane(a, e >> 1), __builtin_amdgcn_readlane(b, e >> 1));
   }
-  // M tiles of BM rows over all experts (incl: up to and with the lane's), and
-  // the record of the expert that holds M tile mtile of them
+  // M tiles of BM rows over all experts (incl: up to and with the lane's)
   __device__ __forceinline__ int tiles(int BM, int& incl) const {
-    int n = 0;
-    each([&](int, int a, int b) { n += (b - a + BM - 1) / BM; });
-    incl = wave_inclusive_scan_i32(n);
+    incl = wave_inclusive_scan_i32((mid - lo + BM - 1) / BM + (hi - mid + BM - 1) / BM);
     return __builtin_amdgcn_readlane(incl, kWave - 1);
   }
+  // the record of the expert that holds M tile mtile
   __device__ __forceinline__ TileRec find(int BM, int mtile, int incl) const {
-    int first = incl, e = 0, f = 0, lo = 0, hi = 0;
-    each([&](int, int a, int b) { first -= (b - a + BM - 1) / BM; });
-    const bool mine = first <= mtile && mtile < incl;
-    each([&](int i, int a, int b) {
-      const int n = (b - a + BM - 1) / BM;
-      if (first <= mtile && mtile < first + n) { e = i; f = first; lo = a; hi = b; }
-      first += n;
-    });
-    const int src = __builtin_ctzll(__ballot(mine));
-    return make_int4(__builtin_amdgcn_readlane(e, src), __builtin_amdgcn_readlane(f, src),
-                     __builtin_amdgcn_readlane(lo, src), __builtin_amdgcn_readlane(hi, src));
+    const int n0 = (mid - lo + BM - 1) / BM, n1 = (hi - mid + BM - 1) / BM, first = incl - n0 - n1;
+    const int src = __builtin_ctzll(__ballot(first <= mtile && mtile < incl));
+    const bool second = mtile >= first + n0;         // (looked at in lane src only)
+    return make_int4(__builtin_amdgcn_readlane(e0 + (second ? 1 : 0), src),
+                     __builtin_amdgcn_readlane(second ? first + n0 : first, src),
+                     __builtin_amdgcn_readlane(second ? mid : lo, src),
+                     __builtin_amdgcn_readlane(second ? hi : mid, src));
   }
-  // the rows of no expert: [0, begin) and [end, R)
+  // first M tile and number of M tiles of expert e
+  __device__ __forceinline__ int2 tiles_of(int e, int BM, int incl) const {
+    const int n0 = (mid - lo + BM - 1) / BM, n1 = (hi - mid + BM - 1) / BM, first = incl - n0 - n1;
+    return make_int2(__builtin_amdgcn_readlane(e & 1 ? first + n0 : first, e >> 1),
+                     __builtin_amdgcn_readlane(e & 1 ? n1 : n0, e >> 1));
+  }
+  // the rows of no expert: [0, x) and [y, R)
   __device__ __forceinline__ int2 covered() const {
-    int lo = R, hi = 0;
-    each([&](int i, int a, int b) {
-      if (i == 0) lo = a;
-      hi = b;
-    });
-    const int last = (E - 1) / C;
-    return make_int2(__builtin_amdgcn_readlane(lo, 0), __builtin_amdgcn_readlane(hi, last));
+    return make_int2(__builtin_amdgcn_readlane(lo, 0),
+                     __builtin_amdgcn_readlane(E & 1 ? mid : hi, (E - 1) >> 1));
   }
 };
 
@@ -326,18 +311,28 @@ __device__ __forceinline__ void store_wave_tile(const f32x16 (&acc)[WTN / 32][WT
   }
 }
 
-// C tile BM x BN by WM x WN waves. OUT: EPI_BF16 or EPI_F32. OCC: waves per
-// SIMD the registers are sized for.
-template <int FORM, int BM, int BN, int WM, int WN, int OCC, int OUT, int AST, int BST>
-__global__ void __launch_bounds__(64 * WM * WN, 1) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
-grouped_kernel(const GroupedArgs P) {
+// LDS of a workgroup: AST stages of the rows operand, BST of the other, each an
+// array of its own, so that the compiler can tell the stage being filled from
+// the one being read.
+struct GroupedLds {
+  u32x4 *a0, *a1, *a2, *a3, *b0, *b1, *b2, *b3;
+};
+#define MOE_GROUPED_LDS(BM, BN, AST, BST)                                                            \
+  static_assert((AST == 2 && (BST == 2 || BST == 3)) || (AST == 4 && BST == 4), "stages");           \
+  __shared__ u32x4 sa0[BM * 8], sb0[BN * 8], sa1[BM * 8], sb1[BN * 8], sb2[BST >= 3 ? BN * 8 : 1];   \
+  __shared__ u32x4 sa2[AST == 4 ? BM * 8 : 1], sa3[AST == 4 ? BM * 8 : 1], sb3[AST == 4 ? BN * 8 : 1]; \
+  const GroupedLds lds{sa0, sa1, sa2, sa3, sb0, sb1, sb2, sb3}
+
+// Workgroup `block` of the `nblocks` of one product: a C tile BM x BN by WM x WN
+// waves. OUT: EPI_BF16 or EPI_F32.
+template <int FORM, int BM, int BN, int WM, int WN, int OUT, int AST, int BST>
+__device__ __forceinline__ void grouped_body(const GroupedArgs& P, int block, int nblocks, const GroupedLds& lds) {
   constexpr int NT = 64 * WM * WN;
   constexpr bool AT = FORM == FORM_TN, BT = FORM != FORM_NT;
-  static_assert(BM * 8 % NT == 0 && BN * 8 % NT == 0, "tile shape");
-  static_assert((AST == 2 && (BST == 2 || BST == 3)) || (AST == 4 && BST == 4), "stages");
   constexpr bool DEEP = AST == 4;
-  __shared__ u32x4 sa0[BM * 8], sb0[BN * 8], sa1[BM * 8], sb1[BN * 8], sb2[BST >= 3 ? BN * 8 : 1];
-  __shared__ u32x4 sa2[DEEP ? BM * 8 : 1], sa3[DEEP ? BM * 8 : 1], sb3[DEEP ? BN * 8 : 1];
+  static_assert(BM * 8 % NT == 0 && BN * 8 % NT == 0, "tile shape");
+  u32x4 *const sa0 = lds.a0, *const sa1 = lds.a1, *const sa2 = lds.a2, *const sa3 = lds.a3;
+  u32x4 *const sb0 = lds.b0, *const sb1 = lds.b1, *const sb2 = lds.b2, *const sb3 = lds.b3;
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -355,14 +350,14 @@ grouped_kernel(const GroupedArgs P) {
       const OffsetScan scan(P.offsets, P.E, P.R, lane);
       int incl;
       const int valid = scan.tiles(P.split, incl) * per;
-      if ((int)blockIdx.x >= valid) return;
-      t = xcd_remap(blockIdx.x, valid);
+      if (block >= valid) return;
+      t = xcd_remap(block, valid);
       e = __builtin_amdgcn_readfirstlane(t / per);       // the piece: C's index
       const TileRec rec = scan.find(P.split, e, incl);
       rg.x = rec.z + (e - rec.y) * P.split;
       rg.y = min(rg.x + P.split, rec.w);
     } else {
-      t = xcd_remap(blockIdx.x, gridDim.x);
+      t = xcd_remap(block, nblocks);
       e = __builtin_amdgcn_readfirstlane(t / per);
       if (P.ranges != nullptr) rg = P.ranges[e];
       else rg = OffsetScan(P.offsets, P.E, P.R, lane).rows(e);
@@ -383,21 +378,21 @@ grouped_kernel(const GroupedArgs P) {
     TileRec rec;
     if (P.tiles != nullptr) {
       valid = *P.n_mtiles * P.ntiles;
-      if ((int)blockIdx.x >= valid) return;
-      t = xcd_remap(blockIdx.x, valid);
+      if (block >= valid) return;
+      t = xcd_remap(block, valid);
       rec = P.tiles[t / P.ntiles];
     } else {
       const OffsetScan scan(P.offsets, P.E, P.R, lane);
-      const int grid = (int)gridDim.x - P.rest_blocks;
-      if ((int)blockIdx.x >= grid) {
+      const int grid = nblocks - P.rest_blocks;
+      if (block >= grid) {
         const int2 c = scan.covered();
-        zero_rest(static_cast<uint16_t*>(P.C), P.ldc, P.N, c.x, c.y, P.R, (int)blockIdx.x - grid, P.rest_blocks, NT);
+        zero_rest(static_cast<uint16_t*>(P.C), P.ldc, P.N, c.x, c.y, P.R, block - grid, P.rest_blocks, NT);
         return;
       }
       int incl;
       valid = scan.tiles(BM, incl) * P.ntiles;
-      if ((int)blockIdx.x >= valid) return;
-      t = xcd_remap(blockIdx.x, valid);
+      if (block >= valid) return;
+      t = xcd_remap(block, valid);
       rec = scan.find(BM, t / P.ntiles, incl);
     }
     const int e = __builtin_amdgcn_readfirstlane(rec.x), first = __builtin_amdgcn_readfirstlane(rec.y);
@@ -612,6 +607,26 @@ grouped_kernel(const GroupedArgs P) {
     if (rows <= 192) { body(Stage<3>{}); return; }
   }
   body(Stage<4>{});
+}
+
+// OCC: waves per SIMD the registers are sized for.
+template <int FORM, int BM, int BN, int WM, int WN, int OCC, int OUT, int AST, int BST>
+__global__ void __launch_bounds__(64 * WM * WN, 1) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
+grouped_kernel(const GroupedArgs P) {
+  MOE_GROUPED_LDS(BM, BN, AST, BST);
+  grouped_body<FORM, BM, BN, WM, WN, OUT, AST, BST>(P, blockIdx.x, gridDim.x, lds);
+}
+
+// Both gradients in one launch: the first g0 workgroups take dx, the others dW
+// (independent sums that leave CUs idle when each runs alone).
+template <int BM, int BN, int WM, int WN, int OCC, int OUT, int AST, int BST>
+__global__ void __launch_bounds__(64 * WM * WN, 1) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
+grouped_grad_kernel(const GroupedArgs DX, const GroupedArgs DW, int g0) {
+  MOE_GROUPED_LDS(BM, BN, AST, BST);
+  if ((int)blockIdx.x < g0)
+    grouped_body<FORM_NN, BM, BN, WM, WN, EPI_BF16, AST, BST>(DX, blockIdx.x, g0, lds);
+  else
+    grouped_body<FORM_TN, BM, BN, WM, WN, OUT, AST, BST>(DW, (int)blockIdx.x - g0, (int)gridDim.x - g0, lds);
 }
 
 }  // namespace moe

@@ -81,10 +81,8 @@ static void launch_form(const GroupedArgs& a, const GroupedPlan& plan, int64_t g
 // then ask for more than the L2 gives: 0.25 us of MFMA a k tile, 32 KB).
 constexpr int64_t kBigTiles = 192, kDeepGrid = 256;
 // Grids of at most this many workgroups find their tiles in the offsets
-// (OffsetScan) and need no table: up to 128 experts, two to a lane (at 512
-// experts and 880 workgroups the table was 11 us faster).
+// (OffsetScan, up to 128 experts) and need no table.
 constexpr int64_t kScanGrid = 1024;
-constexpr int kScanExperts = 128;
 
 static void finish_plan(GroupedPlan& p, int E) {
   p.deep = p.bm == 128 && p.grid <= kDeepGrid;
@@ -137,15 +135,8 @@ __global__ void __launch_bounds__(256) wgrad_join_kernel(const float* __restrict
   const OffsetScan scan(P.offsets, P.E, P.R, lane);
   int incl;
   scan.tiles(P.split, incl);
-  int first = 0, n = 0, at = incl;
-  scan.each([&](int, int a, int b) { at -= (b - a + P.split - 1) / P.split; });
-  scan.each([&](int i, int a, int b) {
-    const int c = (b - a + P.split - 1) / P.split;
-    if (i == e) { first = at; n = c; }
-    at += c;
-  });
-  first = __builtin_amdgcn_readlane(first, e / scan.C);
-  n = __builtin_amdgcn_readlane(n, e / scan.C);
+  const int2 own = scan.tiles_of(e, P.split, incl);
+  const int first = own.x, n = own.y;
   if (n == 0 && P.accumulate) return;
   const int64_t i = ((int64_t)(blockIdx.x - e * blocks) * 256 + threadIdx.x) * 4;
   if (i >= size) return;
@@ -168,8 +159,7 @@ __global__ void __launch_bounds__(256) wgrad_join_kernel(const float* __restrict
   }
 }
 
-hipError_t launch_grouped_rows(const GroupedProduct& p, const GroupedPlan& plan, const GroupedScratch& s, bool rest,
-                               hipStream_t st) {
+static GroupedArgs rows_args(const GroupedProduct& p, const GroupedPlan& plan, const GroupedScratch& s, bool rest) {
   GroupedArgs a{};
   a.A = p.A;
   a.B = p.B;
@@ -187,22 +177,20 @@ hipError_t launch_grouped_rows(const GroupedProduct& p, const GroupedPlan& plan,
   a.R = (int)p.R;
   a.rest_blocks = plan.scan && rest ? kScanRestBlocks : 0;
   a.ntiles = plan.ntiles;
-  const int64_t grid = plan.grid + a.rest_blocks;
-  if (p.transposed_b) launch_form<FORM_NN, EPI_BF16>(a, plan, grid, st);
-  else launch_form<FORM_NT, EPI_BF16>(a, plan, grid, st);
-  return hipGetLastError();
+  return a;
 }
 
-hipError_t launch_grouped_wgrad(const GroupedProduct& p, int M, bool f32, bool accumulate, const GroupedPlan& plan,
-                                const GroupedScratch& s, hipStream_t st) {
+// (a split gradient: of the launch that sums the pieces)
+static GroupedArgs wgrad_args(const GroupedProduct& p, int M, bool accumulate, const GroupedPlan& plan,
+                              const GroupedScratch& s) {
   GroupedArgs a{};
   a.A = p.A;
   a.B = p.B;
-  a.C = p.C;
+  a.C = plan.split ? s.partial : p.C;
   a.lda = p.lda;
   a.ldb = p.ldb;
-  a.ldc = p.ldc;
-  a.c_estride = p.estride;
+  a.ldc = plan.split ? p.N : p.ldc;
+  a.c_estride = plan.split ? (int64_t)M * p.N : p.estride;
   a.M = M;
   a.N = p.N;
   a.ranges = plan.scan ? nullptr : s.ranges;
@@ -211,28 +199,65 @@ hipError_t launch_grouped_wgrad(const GroupedProduct& p, int M, bool f32, bool a
   a.R = (int)p.R;
   a.mtiles = plan.mtiles;
   a.ntiles = plan.ntiles;
+  a.split = plan.split;
+  a.accumulate = accumulate && !plan.split;
+  return a;
+}
+
+static hipError_t launch_join(const GroupedProduct& p, int M, bool f32, bool accumulate, const GroupedPlan& plan,
+                              const GroupedScratch& s, hipStream_t st) {
+  GroupedArgs a = wgrad_args(p, M, false, plan, s);
+  a.C = p.C;
   a.accumulate = accumulate;
-  if (plan.split) {
-    GroupedArgs q = a;
-    q.split = plan.split;
-    q.C = s.partial;
-    q.ldc = p.N;
-    q.c_estride = (int64_t)M * p.N;
-    q.accumulate = 0;
-    launch_form<FORM_TN, EPI_F32>(q, plan, plan.grid, st);
-    const hipError_t err = hipGetLastError();
-    if (err != hipSuccess) return err;
-    a.split = plan.split;
-    const int64_t size = (int64_t)M * p.N;
-    const int blocks = (int)((size + 1023) / 1024);
-    const dim3 grid((unsigned)((int64_t)p.E * blocks));
-    if (f32) hipLaunchKernelGGL(wgrad_join_kernel<EPI_F32>, grid, dim3(256), 0, st, s.partial, a, size, blocks);
-    else hipLaunchKernelGGL(wgrad_join_kernel<EPI_BF16>, grid, dim3(256), 0, st, s.partial, a, size, blocks);
-    return hipGetLastError();
-  }
-  if (f32) launch_form<FORM_TN, EPI_F32>(a, plan, plan.grid, st);
-  else launch_form<FORM_TN, EPI_BF16>(a, plan, plan.grid, st);
+  const int64_t size = (int64_t)M * p.N;
+  const int blocks = (int)((size + 1023) / 1024);
+  const dim3 grid((unsigned)((int64_t)p.E * blocks));
+  if (f32) hipLaunchKernelGGL(wgrad_join_kernel<EPI_F32>, grid, dim3(256), 0, st, s.partial, a, size, blocks);
+  else hipLaunchKernelGGL(wgrad_join_kernel<EPI_BF16>, grid, dim3(256), 0, st, s.partial, a, size, blocks);
   return hipGetLastError();
+}
+
+hipError_t launch_grouped_rows(const GroupedProduct& p, const GroupedPlan& plan, const GroupedScratch& s, bool rest,
+                               hipStream_t st) {
+  const GroupedArgs a = rows_args(p, plan, s, rest);
+  const int64_t grid = plan.grid + a.rest_blocks;
+  if (p.transposed_b) launch_form<FORM_NN, EPI_BF16>(a, plan, grid, st);
+  else launch_form<FORM_NT, EPI_BF16>(a, plan, grid, st);
+  return hipGetLastError();
+}
+
+hipError_t launch_grouped_wgrad(const GroupedProduct& p, int M, bool f32, bool accumulate, const GroupedPlan& plan,
+                                const GroupedScratch& s, hipStream_t st) {
+  const GroupedArgs a = wgrad_args(p, M, accumulate, plan, s);
+  if (f32 || plan.split) launch_form<FORM_TN, EPI_F32>(a, plan, plan.grid, st);
+  else launch_form<FORM_TN, EPI_BF16>(a, plan, plan.grid, st);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !plan.split) return e;
+  return launch_join(p, M, f32, accumulate, plan, s, st);
+}
+
+bool grouped_grad_in_one(const GroupedPlan& rows, const GroupedPlan& wgrad) {
+  return rows.bm == 128 && wgrad.bm == 128 && rows.scan && wgrad.scan;
+}
+
+hipError_t launch_grouped_grad(const GroupedProduct& dx, const GroupedPlan& rows, bool rest, const GroupedProduct& dw,
+                               const GroupedPlan& wgrad, int M, bool f32, bool accumulate, const GroupedScratch& s,
+                               hipStream_t st) {
+  const GroupedArgs a = rows_args(dx, rows, s, rest), b = wgrad_args(dw, M, accumulate, wgrad, s);
+  const int g0 = (int)rows.grid + a.rest_blocks;
+  const dim3 grid((unsigned)(g0 + wgrad.grid));
+  const bool deep = rows.grid + wgrad.grid <= kDeepGrid, wide = f32 || wgrad.split;
+  if (deep && wide)
+    hipLaunchKernelGGL((grouped_grad_kernel<128, 128, 2, 2, 1, EPI_F32, 4, 4>), grid, dim3(256), 0, st, a, b, g0);
+  else if (deep)
+    hipLaunchKernelGGL((grouped_grad_kernel<128, 128, 2, 2, 1, EPI_BF16, 4, 4>), grid, dim3(256), 0, st, a, b, g0);
+  else if (wide)
+    hipLaunchKernelGGL((grouped_grad_kernel<128, 128, 2, 2, 2, EPI_F32, 2, 2>), grid, dim3(256), 0, st, a, b, g0);
+  else
+    hipLaunchKernelGGL((grouped_grad_kernel<128, 128, 2, 2, 2, EPI_BF16, 2, 2>), grid, dim3(256), 0, st, a, b, g0);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !wgrad.split) return e;
+  return launch_join(dw, M, f32, accumulate, wgrad, s, st);
 }
 
 }  // namespace moe

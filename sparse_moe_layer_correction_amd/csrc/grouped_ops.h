@@ -56,6 +56,12 @@ hipError_t launch_grouped_rows(const GroupedProduct& p, const GroupedPlan& plan,
 hipError_t launch_grouped_wgrad(const GroupedProduct& p, int M, bool f32, bool accumulate, const GroupedPlan& plan,
                                 const GroupedScratch& s, hipStream_t st);
 
+// dx and dW in one launch, where both are small
+bool grouped_grad_in_one(const GroupedPlan& rows, const GroupedPlan& wgrad);
+hipError_t launch_grouped_grad(const GroupedProduct& dx, const GroupedPlan& rows, bool rest, const GroupedProduct& dw,
+                               const GroupedPlan& wgrad, int M, bool f32, bool accumulate, const GroupedScratch& s,
+                               hipStream_t st);
+
 // E4M3 codes, one scale per 128 (fp8.h)
 struct Fp8Args {
   const uint8_t* A;            // [R, K] codes of the rows
@@ -77,11 +83,10 @@ hipError_t launch_fp8_blocks(const uint16_t* w, int64_t count, int N, int K, uin
                              hipStream_t st);
 hipError_t launch_grouped_fp8(const Fp8Args& a, const GroupedPlan& plan, hipStream_t st);
 
-// Gradient tensors of one launch; entry i's chunks of kGradChunk elements are
+// Gradient tensors of one launch; entry i's chunks of 2^chunk_log2 elements are
 // first[i] .. first[i + 1] of the launch's (the last entry's end at chunks). The
 // table is a kernel argument: few tensors take the short one.
 constexpr int kGradTableSize = 120, kGradShortTable = 16;
-constexpr int kGradChunk = 1 << 15;
 template <int SIZE>
 struct GradTableOf {
   const void* src[SIZE];
@@ -89,7 +94,7 @@ struct GradTableOf {
   int64_t n[SIZE];
   int first[SIZE];
   uint32_t f32[(SIZE + 31) / 32];   // bit i: entry i is fp32, else bf16
-  int count, chunks;
+  int count, chunks, chunk_log2;
 };
 typedef GradTableOf<kGradTableSize> GradTable;
 static_assert(sizeof(GradTable) <= 4000, "kernel arguments");

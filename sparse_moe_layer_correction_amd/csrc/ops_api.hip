@@ -152,15 +152,13 @@ int moe_grouped_matmul_grad(const moe_grouped_dims* dims, const uint16_t* dy, co
   const RestRows rest{run_dx && !rows.scan && d.zero_rest ? dx : nullptr, d.lddx, d.K};
   if (plans.table_bm > 0)
     if (launch_grouped_tiles(offsets, d.E, (int)d.R, rows.bm, s, rest, stream) != hipSuccess) return MOE_ERR_HIP;
-  if (run_dx) {
-    const GroupedProduct p{dy, w, dx, d.ldy, d.ldw, d.lddx, d.w_stride, d.R, d.E, d.K, d.N, true, offsets};
-    if (launch_grouped_rows(p, rows, s, d.zero_rest != 0, stream) != hipSuccess) return MOE_ERR_HIP;
-  }
-  if (dw) {
-    const GroupedProduct p{dy, x, dw, d.ldy, d.ldx, d.K, (int64_t)d.N * d.K, d.R, d.E, d.K, 0, true, offsets};
-    if (launch_grouped_wgrad(p, d.N, dw_dtype == MOE_FP32, accumulate != 0, wg, s, stream) != hipSuccess)
-      return MOE_ERR_HIP;
-  }
+  const GroupedProduct px{dy, w, dx, d.ldy, d.ldw, d.lddx, d.w_stride, d.R, d.E, d.K, d.N, true, offsets};
+  const GroupedProduct pw{dy, x, dw, d.ldy, d.ldx, d.K, (int64_t)d.N * d.K, d.R, d.E, d.K, 0, true, offsets};
+  const bool f32 = dw_dtype == MOE_FP32, rest_rows = d.zero_rest != 0;
+  if (run_dx && dw && grouped_grad_in_one(rows, wg))
+    return hip_status(launch_grouped_grad(px, rows, rest_rows, pw, wg, d.N, f32, accumulate != 0, s, stream));
+  if (run_dx && launch_grouped_rows(px, rows, s, rest_rows, stream) != hipSuccess) return MOE_ERR_HIP;
+  if (dw && launch_grouped_wgrad(pw, d.N, f32, accumulate != 0, wg, s, stream) != hipSuccess) return MOE_ERR_HIP;
   return MOE_OK;
 }
 
@@ -264,7 +262,18 @@ namespace {
 constexpr int kGradBlocks = 2048;
 
 size_t dtype_size(int32_t dt) { return dt == MOE_FP32 ? 4 : 2; }
-int64_t chunks_of(int64_t n) { return (n + kGradChunk - 1) / kGradChunk; }
+int64_t chunks_of(int64_t n, int log2) { return (n + ((int64_t)1 << log2) - 1) >> log2; }
+
+// Chunks of 2^11 elements (8 of a thread's 256 each) for few, so that they spread
+// over the CUs, up to 2^20 for many: about 8 to a workgroup, which evens out the
+// workgroups' shares.
+int chunk_log2(const moe_grad_tensor* t, int32_t count) {
+  int64_t total = 0;
+  for (int32_t i = 0; i < count; ++i) total += t[i].n;
+  int log2 = 11;
+  while (log2 < 20 && (total >> log2) > (int64_t)8 * kGradBlocks) ++log2;
+  return log2;
+}
 
 int check_tensors(const moe_grad_tensor* t, int32_t count) {
   if (count < 0 || (count > 0 && t == nullptr)) return MOE_ERR_INVALID;
@@ -285,6 +294,7 @@ int check_tensors(const moe_grad_tensor* t, int32_t count) {
 template <typename F>
 int for_tables(const moe_grad_tensor* t, int32_t count, bool reverse, F&& f) {
   GradTable tab;
+  tab.chunk_log2 = chunk_log2(t, count);
   auto clear = [&]() {
     tab.count = tab.chunks = 0;
     for (uint32_t& w : tab.f32) w = 0;
@@ -299,7 +309,7 @@ int for_tables(const moe_grad_tensor* t, int32_t count, bool reverse, F&& f) {
   for (int32_t j = 0; j < count; ++j) {
     const moe_grad_tensor& g = t[reverse ? count - 1 - j : j];
     if (g.n == 0) continue;
-    const int64_t c = chunks_of(g.n);                // at most 2^25
+    const int64_t c = chunks_of(g.n, tab.chunk_log2);   // at most 2^20 + 1
     if (tab.count == kGradTableSize || tab.chunks + c > 0x7FFFFFFF) {
       const int rc = flush();
       if (rc != MOE_OK) return rc;
@@ -320,11 +330,12 @@ int table_blocks(const GradTable& t) { return std::min(t.chunks, kGradBlocks); }
 // the partial sums' number: the workgroups of all launches
 size_t partials_of(const moe_grad_tensor* t, int32_t count) {
   size_t n = 0;
+  const int log2 = chunk_log2(t, count);
   int in_table = 0;
   int64_t chunks = 0;
   for (int32_t i = 0; i < count; ++i) {
     if (t[i].n == 0) continue;
-    const int64_t c = chunks_of(t[i].n);
+    const int64_t c = chunks_of(t[i].n, log2);
     if (in_table == kGradTableSize || chunks + c > 0x7FFFFFFF) {
       n += (size_t)std::min<int64_t>(chunks, kGradBlocks);
       in_table = 0;
