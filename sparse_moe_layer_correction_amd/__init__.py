@@ -18,6 +18,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+from array import array
 from dataclasses import dataclass
 from typing import Dict, Optional
 
@@ -811,39 +812,53 @@ def grouped_matmul_fp8(x, w_codes, w_scale, offsets, *, x_scale=None, out=None, 
 # the end of a training step: global gradient norm and clipping
 # ----------------------------------------------------------------------------
 
-def _grad_table(grads, out):
-    """The moe_grad_tensor array of ``grads`` (as a pointer and its storage), their number, the first tensor."""
+def _refuse_grads(grads, outs, index):
+    """Raises for the first tensor that a moe_grad_tensor array cannot take."""
     torch = _torch()
-    grads = list(grads)
-    outs = grads if out is None else list(out)
-    if len(outs) != len(grads):
-        raise ValueError(f"out must hold one tensor for each of the {len(grads)} gradients, got {len(outs)}")
-    if not grads:
-        raise ValueError("grads must hold at least one tensor")
-    Tensor, bf16, fp32 = torch.Tensor, torch.bfloat16, torch.float32
-    index = grads[0].get_device() if isinstance(grads[0], Tensor) else -1
-    words = []                       # four 64-bit words an entry: grad, out, n, dtype (and its padding)
-    for i, g in enumerate(grads):
-        if not isinstance(g, Tensor):
+    for i, (g, o) in enumerate(zip(grads, outs)):
+        if not isinstance(g, torch.Tensor):
             raise TypeError(f"gradient {i} must be a torch tensor")
-        dt = g.dtype
-        if dt is not bf16 and dt is not fp32:
-            raise TypeError(f"gradient {i} must be bf16 or fp32, got {dt}")
-        if g.get_device() != index or index < 0:
+        if g.dtype not in (torch.bfloat16, torch.float32):
+            raise TypeError(f"gradient {i} must be bf16 or fp32, got {g.dtype}")
+        if index < 0 or g.get_device() != index:
             raise ValueError(f"gradient {i} must be on the GPU of the first one, got {g.device}")
         if not g.is_contiguous():
             raise ValueError(f"gradient {i} must be contiguous")
-        n = g.numel()
-        o = outs[i]
-        at = 0
-        if o is not g:
-            if not isinstance(o, Tensor) or o.dtype is not dt or o.numel() != n or o.get_device() != index \
-                    or not o.is_contiguous():
-                raise ValueError(f"out {i} must be a contiguous {dt} tensor of {n} elements on {g.device}")
-            at = o.data_ptr()
-        words += (g.data_ptr(), at, n, 0 if dt is bf16 else 1)
-    raw = (ctypes.c_int64 * len(words))(*words)
-    return ctypes.cast(raw, ctypes.POINTER(_GradTensor)), raw, len(grads), grads[0]
+        if not isinstance(o, torch.Tensor) or o.dtype != g.dtype or o.numel() != g.numel() \
+                or o.get_device() != index or not o.is_contiguous():
+            raise ValueError(f"out {i} must be a contiguous {g.dtype} tensor of {g.numel()} elements on {g.device}")
+
+
+def _grad_table(grads, outs):
+    """The moe_grad_tensor array of ``grads`` (as a pointer and its storage), their number, the first
+    tensor. Whole lists at a time: a step has hundreds of tensors, and a check of each by
+    itself costs more than the kernels of the small ones."""
+    torch = _torch()
+    T = torch.Tensor
+    n = len(grads)
+    if outs is not None and len(outs) != n:
+        raise ValueError(f"out must hold one tensor for each of the {n} gradients, got {len(outs)}")
+    if n == 0:
+        raise ValueError("grads must hold at least one tensor")
+    every = grads if outs is None else grads + outs
+    index = grads[0].get_device() if isinstance(grads[0], T) else -1
+    if index < 0 or not all(isinstance(t, T) for t in every):
+        _refuse_grads(grads, grads if outs is None else outs, index)
+    kinds = [t.dtype for t in every]
+    sizes = list(map(T.numel, every))
+    if set(kinds) - {torch.bfloat16, torch.float32} or set(map(T.get_device, every)) != {index} \
+            or not all(map(T.is_contiguous, every)) \
+            or (outs is not None and (kinds[:n] != kinds[n:] or sizes[:n] != sizes[n:])):
+        _refuse_grads(grads, grads if outs is None else outs, index)
+    # four 64-bit words an entry: grad, out, n, dtype (and its padding)
+    at = array("q", map(T.data_ptr, every))
+    raw = array("q", bytes(32 * n))
+    raw[0::4] = at[:n]
+    if outs is not None:
+        raw[1::4] = at[n:]
+    raw[2::4] = array("q", sizes[:n])
+    raw[3::4] = array("q", [k is torch.float32 for k in kinds[:n]])
+    return ctypes.cast(raw.buffer_info()[0], ctypes.POINTER(_GradTensor)), raw, n, grads[0]
 
 
 def _grad_call(fn, tab, n, index, ws, *args):
