@@ -33,7 +33,7 @@ constexpr int kWaitLgkm0 = 0xF | (0x7 << 4) | (3 << 14);
 // scales follow, and the next tile's first fragments are read. Every load of
 // codes then has one and a half k tiles to land, and each barrier waits only
 // for what is read next.
-template <int BM, int BN, int WM, int WN, int OCC>
+template <int BM, int BN, int WM, int WN, int OCC, int OUT>
 __global__ void __launch_bounds__(64 * WM * WN, 1) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
 grouped_fp8_kernel(const Fp8Args P) {
   constexpr int NT = 64 * WM * WN;
@@ -48,33 +48,47 @@ grouped_fp8_kernel(const Fp8Args P) {
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wave_m = wave % WM, wave_n = wave / WM;
 
+  // a split reduction: piece s of ksplit sums klen codes (blocks of 128) into C + s * c_stride (fp32)
+  int block = blockIdx.x, nblocks = gridDim.x, kt0 = 0, kb = P.kb;
+  int64_t c_base = 0;
+  if (P.ksplit > 1) {
+    nblocks /= P.ksplit;
+    const int piece = block / nblocks;
+    block -= piece * nblocks;
+    kt0 = piece * P.klen;
+    kb = min(P.klen, P.kb - kt0);
+    c_base = piece * P.c_stride;
+  }
   int valid, t;
   TileRec rec;
   if (P.tiles != nullptr) {
     valid = *P.n_mtiles * P.ntiles;
-    if ((int)blockIdx.x >= valid) return;
-    t = xcd_remap(blockIdx.x, valid);
+    if (block >= valid) return;
+    t = xcd_remap(block, valid);
     rec = P.tiles[t / P.ntiles];
   } else {
-    const OffsetScan scan(P.offsets, P.E, (int)P.R, lane);
-    const int grid = (int)gridDim.x - P.rest_blocks;
-    if ((int)blockIdx.x >= grid) {
-      const int2 c = scan.covered();
-      zero_rest(P.C, P.ldc, P.N, c.x, c.y, (int)P.R, (int)blockIdx.x - grid, P.rest_blocks, NT);
-      return;
-    }
-    int incl;
-    valid = scan.tiles(BM, incl) * P.ntiles;
-    if ((int)blockIdx.x >= valid) return;
-    t = xcd_remap(blockIdx.x, valid);
-    rec = scan.find(BM, t / P.ntiles, incl);
+    const bool mine = with_scan(P.offsets, P.E, (int)P.R, lane, [&](const auto& scan) {
+      const int grid = nblocks - P.rest_blocks;
+      if (block >= grid) {
+        const int2 c = scan.covered();
+        zero_rest(static_cast<uint16_t*>(P.C), P.ldc, P.N, c.x, c.y, (int)P.R, block - grid, P.rest_blocks, NT);
+        return false;
+      }
+      int incl;
+      valid = scan.tiles(BM, incl) * P.ntiles;
+      if (block >= valid) return false;
+      t = xcd_remap(block, valid);
+      rec = scan.find(BM, t / P.ntiles, incl);
+      return true;
+    });
+    if (!mine) return;
   }
   const int e = __builtin_amdgcn_readfirstlane(rec.x), first = __builtin_amdgcn_readfirstlane(rec.y);
   const int lo = __builtin_amdgcn_readfirstlane(rec.z), hi = __builtin_amdgcn_readfirstlane(rec.w);
   int mt, nt;
   grouped_tile_order(t - first * P.ntiles, (hi - lo + BM - 1) / BM, (hi - lo) / BM, P.ntiles, 8, mt, nt);
   const int m0 = __builtin_amdgcn_readfirstlane(lo + mt * BM), n0 = __builtin_amdgcn_readfirstlane(nt * BN);
-  const int K2 = P.K / 2;                              // the loads count pairs of codes
+  const int ld2 = P.K / 2, K2 = min(P.K - kt0 * 128, kb * 128) / 2;   // the loads count pairs of codes
 
   // HQ: the tile's height in quarters of BM (1, 2 or 4: an expert's last tile may be short)
   auto body = [&](auto height) __attribute__((always_inline)) {
@@ -88,10 +102,11 @@ grouped_fp8_kernel(const Fp8Args P) {
     constexpr int NA = LoadA::NL, NB = BN * 8 / NT;
     LoadA la, lah;
     OperandLoad<BN, false, NT> lb;
-    const uint16_t* rows8 = reinterpret_cast<const uint16_t*>(P.A + (int64_t)m0 * P.K);
-    la.init(rows8, K2, hi - m0, K2, wave, lane);
-    if constexpr (HALVES) lah.init(rows8, K2, hi - m0, K2, wave, lane, WTM / 2);
-    lb.init(reinterpret_cast<const uint16_t*>(P.B + ((int64_t)e * P.N + n0) * P.K), K2, P.N - n0, K2, wave, lane);
+    const uint16_t* rows8 = reinterpret_cast<const uint16_t*>(P.A + (int64_t)m0 * P.K + kt0 * 128);
+    la.init(rows8, ld2, hi - m0, K2, wave, lane);
+    if constexpr (HALVES) lah.init(rows8, ld2, hi - m0, K2, wave, lane, WTM / 2);
+    lb.init(reinterpret_cast<const uint16_t*>(P.B + ((int64_t)e * P.N + n0) * P.K + kt0 * 128), ld2, P.N - n0, K2, wave,
+            lane);
 
     // a k tile's row scales: one dword per lane, 64 rows a wave (waves beyond
     // the tile's rows repeat others'); rows past the end repeat the last one
@@ -99,16 +114,16 @@ grouped_fp8_kernel(const Fp8Args P) {
     const int srow = (wave % SW) * 64;
     const uint32_t sofs = (uint32_t)min(srow + lane, hi - 1 - m0) * 4;
     auto issue_scales = [&](float* st, int kt) {
-      const bool live = kt < P.kb;
+      const bool live = kt < kb;
       const __amdgpu_buffer_rsrc_t r =
-          make_rsrc(uniform_ptr(reinterpret_cast<const uint16_t*>(P.sx + (live ? (int64_t)kt * P.R : 0) + m0)),
+          make_rsrc(uniform_ptr(reinterpret_cast<const uint16_t*>(P.sx + (int64_t)(kt0 + (live ? kt : 0)) * P.R + m0)),
                     live ? kRsrc2G : 0);
       __builtin_amdgcn_raw_ptr_buffer_load_lds(r, (lds_void_ptr)&st[srow], 4, (int)sofs, 0, 0, 0);
     };
     // the wave's weight scales, one a k tile (scalar loads, through the constant address space)
     typedef const __attribute__((address_space(4))) float* scale_ptr;
     const scale_ptr sw = (scale_ptr)(uintptr_t)uniform_ptr(reinterpret_cast<const uint16_t*>(
-        P.sw + ((int64_t)e * P.nb + min((n0 + wave_n * WTN) / 128, P.nb - 1)) * P.kb));
+        P.sw + ((int64_t)e * P.nb + min((n0 + wave_n * WTN) / 128, P.nb - 1)) * P.kb + kt0));
 
     f32x4 acc[TM][TN];
 #pragma unroll
@@ -149,7 +164,7 @@ grouped_fp8_kernel(const Fp8Args P) {
       for (int m = 0; m < TM; ++m) {
         i32x8 fn;
         float sn;
-        if (m == TM / 2) wn = sw[min(kt + 1, P.kb - 1)];
+        if (m == TM / 2) wn = sw[min(kt + 1, kb - 1)];
         if (m + 1 == TM / 2) {
           // (unsplit rows: the last barrier waited for the whole tile)
           __builtin_amdgcn_s_waitcnt(HALVES ? wait_lgkm0(NB + 2 * NA + 1) : kWaitLgkm0);
@@ -212,11 +227,11 @@ grouped_fp8_kernel(const Fp8Args P) {
 #pragma unroll
     for (int n = 0; n < TN; ++n) fb[n] = frag_b(sb0, n);
     int kt = 0;
-    for (; kt + 1 < P.kb; kt += 2) {
+    for (; kt + 1 < kb; kt += 2) {
       step(kt, sa0, sa0h, sb0, sc0, sa1, sb1, sc1);
       step(kt + 1, sa1, sa1h, sb1, sc1, sa0, sb0, sc0);
     }
-    if (kt < P.kb) step(kt, sa0, sa0h, sb0, sc0, sa1, sb1, sc1);
+    if (kt < kb) step(kt, sa0, sa0h, sb0, sc0, sa1, sb1, sc1);
 #pragma unroll
     for (int n = 0; n < TN; ++n)
 #pragma unroll
@@ -224,6 +239,20 @@ grouped_fp8_kernel(const Fp8Args P) {
     MOE_WAIT_VMCNT(0);
     __syncthreads();
 
+    if constexpr (OUT == EPI_F32) {
+      // pieces: straight from the registers (16 bytes of 16 rows a store; few and small)
+      float* out = static_cast<float*>(P.C) + c_base;
+#pragma unroll
+      for (int m = 0; m < TM; ++m) {
+        const int row = m0 + wave_m * WTM + m * 16 + r16;
+#pragma unroll
+        for (int n = 0; n < TN; ++n) {
+          const int col = n0 + wave_n * WTN + n * 16 + 4 * (lane >> 4);
+          if (row < hi && col < P.N) *reinterpret_cast<f32x4*>(out + (int64_t)row * P.ldc + col) = acc[m][n];
+        }
+      }
+      return;
+    }
     // through LDS to whole rows of the wave tile, as store_wave_tile
     constexpr int CPW = WTN / 8, RPI = 64 / CPW, NRB = WTM / RPI, SB = WTM * WTN * 2;
     constexpr int APER = BM * 64 / SB, BPER = BN * 128 / SB;     // wave tiles in a row half, in a weight stage
@@ -255,7 +284,7 @@ grouped_fp8_kernel(const Fp8Args P) {
     }
     const int mw = m0 + wave_m * WTM, nw = n0 + wave_n * WTN;
     if (nw + c * 8 < P.N) {
-      uint16_t* out = P.C + (int64_t)(mw + r0) * P.ldc + nw + c * 8;
+      uint16_t* out = static_cast<uint16_t*>(P.C) + (int64_t)(mw + r0) * P.ldc + nw + c * 8;
 #pragma unroll
       for (int i = 0; i < NRB; ++i, out += RPI * P.ldc)
         if (mw + i * RPI + r0 < hi) *reinterpret_cast<u32x4*>(out) = rb[i];

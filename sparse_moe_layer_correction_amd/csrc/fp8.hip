@@ -142,11 +142,13 @@ hipError_t launch_fp8_blocks(const uint16_t* w, int64_t count, int N, int K, uin
 }
 
 hipError_t launch_grouped_fp8(const Fp8Args& a, const GroupedPlan& plan, hipStream_t st) {
-  const dim3 grid((unsigned)plan.grid + a.rest_blocks);
-  if (plan.bm == 256)
-    hipLaunchKernelGGL((grouped_fp8_kernel<256, 256, 2, 4, 2>), grid, dim3(512), 0, st, a);
+  const dim3 grid((unsigned)(plan.grid * std::max(1, plan.ksplit)) + a.rest_blocks);
+  if (plan.ksplit)
+    hipLaunchKernelGGL((grouped_fp8_kernel<128, 128, 2, 2, 2, EPI_F32>), grid, dim3(256), 0, st, a);
+  else if (plan.bm == 256)
+    hipLaunchKernelGGL((grouped_fp8_kernel<256, 256, 2, 4, 2, EPI_BF16>), grid, dim3(512), 0, st, a);
   else
-    hipLaunchKernelGGL((grouped_fp8_kernel<128, 128, 2, 2, 2>), grid, dim3(256), 0, st, a);
+    hipLaunchKernelGGL((grouped_fp8_kernel<128, 128, 2, 2, 2, EPI_BF16>), grid, dim3(256), 0, st, a);
   return hipGetLastError();
 }
 

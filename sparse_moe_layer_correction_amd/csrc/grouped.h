@@ -40,68 +40,97 @@ struct GroupedArgs {
   int rest_blocks;             // without a table: the grid's last workgroups zero the rows of no expert
   int mtiles, ntiles;          // wgrad: tiles of one expert's C; else ntiles = column tiles
   int accumulate;              // wgrad: add to what C holds
+  int ksplit, klen;            // forward, dgrad: pieces of the reduction (0 or 1: none) and their length; piece
+                               //   s's fp32 sums go to C + s * c_estride
   int split;                   // wgrad: rows of a piece (0: an expert's rows are one sum); piece i's
                                //   fp32 sums go to C + i * c_estride
 };
 
-// Finds, in one wave and from the offsets alone, what the tile table holds, for
-// up to 128 experts: lane l has the experts 2 l and 2 l + 1. One round of loads
-// and two scans over the lanes, against a launch of its own for the table: taken
-// for the grids of few workgroups (grouped.hip).
-constexpr int kScanExperts = 2 * kWave;
+// Finds, in one wave and from the offsets alone, what the tile table holds: lane
+// l has the Q experts from Q l on (Q = 2 for up to 128 experts, 16 for 1024). One
+// round of loads and two scans over the lanes, against a launch of its own for
+// the table: taken for the grids of few workgroups (grouped.hip).
+template <int Q>
 struct OffsetScan {
-  int E, e0;
-  int lo, mid, hi;     // the lane's experts have the rows [lo, mid) and [mid, hi); none past E
-  __device__ __forceinline__ OffsetScan(const int32_t* offsets, int E_, int R, int lane) : E(E_), e0(2 * lane) {
-    auto at = [&](int i) { return min(max(offsets[min(i, E_)], 0), R); };
-    lo = at(e0);
-    mid = max(lo, at(e0 + 1));
-    hi = at(e0 + 2);
-    int v = mid;                                     // the running maximum up to the lane's second start
+  int e0;
+  int s[Q + 1];        // expert e0 + j has the rows [s[j], s[j + 1]); none past the last expert
+  __device__ __forceinline__ OffsetScan(const int32_t* offsets, int E, int R, int lane) : e0(Q * lane) {
+#pragma unroll
+    for (int j = 0; j <= Q; ++j) s[j] = min(max(offsets[min(e0 + j, E)], 0), R);
+#pragma unroll
+    for (int j = 1; j <= Q; ++j) s[j] = max(s[j], s[j - 1]);
+    int v = s[Q - 1];                                // the running maximum up to the lane's last start
 #pragma unroll
     for (int d = 1; d < kWave; d <<= 1) {
       const int o = __shfl_up(v, d, kWave);
       if (lane >= d) v = max(v, o);
     }
     const int before = __shfl_up(v, 1, kWave);
-    if (lane > 0) lo = max(lo, before);
-    mid = v;
-    hi = max(hi, mid);
-    if (e0 >= E) mid = hi = lo;                      // (past the end every offset read is the last one)
-    else if (e0 + 1 >= E) hi = mid;
+    if (lane > 0) {
+#pragma unroll
+      for (int j = 0; j <= Q; ++j) s[j] = max(s[j], before);
+    }
   }
+  __device__ __forceinline__ int tiles_at(int j, int BM) const { return (s[j + 1] - s[j] + BM - 1) / BM; }
   // rows of expert e, the same in every lane
   __device__ __forceinline__ int2 rows(int e) const {
-    const int a = e & 1 ? mid : lo, b = e & 1 ? hi : mid;
-    return make_int2(__builtin_amdgcn_readlane(a, e >> 1), __builtin_amdgcn_readlane(b, e >> 1));
+    int a = 0, b = 0;
+#pragma unroll
+    for (int j = 0; j < Q; ++j)
+      if (e % Q == j) { a = s[j]; b = s[j + 1]; }
+    return make_int2(__builtin_amdgcn_readlane(a, e / Q), __builtin_amdgcn_readlane(b, e / Q));
   }
   // M tiles of BM rows over all experts (incl: up to and with the lane's)
   __device__ __forceinline__ int tiles(int BM, int& incl) const {
-    incl = wave_inclusive_scan_i32((mid - lo + BM - 1) / BM + (hi - mid + BM - 1) / BM);
+    int n = 0;
+#pragma unroll
+    for (int j = 0; j < Q; ++j) n += tiles_at(j, BM);
+    incl = wave_inclusive_scan_i32(n);
     return __builtin_amdgcn_readlane(incl, kWave - 1);
+  }
+  // the lane's first M tile
+  __device__ __forceinline__ int first_tile(int BM, int incl) const {
+#pragma unroll
+    for (int j = 0; j < Q; ++j) incl -= tiles_at(j, BM);
+    return incl;
   }
   // the record of the expert that holds M tile mtile
   __device__ __forceinline__ TileRec find(int BM, int mtile, int incl) const {
-    const int n0 = (mid - lo + BM - 1) / BM, n1 = (hi - mid + BM - 1) / BM, first = incl - n0 - n1;
+    int first = first_tile(BM, incl);
     const int src = __builtin_ctzll(__ballot(first <= mtile && mtile < incl));
-    const bool second = mtile >= first + n0;         // (looked at in lane src only)
-    return make_int4(__builtin_amdgcn_readlane(e0 + (second ? 1 : 0), src),
-                     __builtin_amdgcn_readlane(second ? first + n0 : first, src),
-                     __builtin_amdgcn_readlane(second ? mid : lo, src),
-                     __builtin_amdgcn_readlane(second ? hi : mid, src));
+    int e = 0, f = 0, lo = 0, hi = 0;                // (looked at in lane src only)
+#pragma unroll
+    for (int j = 0; j < Q; ++j) {
+      const int n = tiles_at(j, BM);
+      if (first <= mtile && mtile < first + n) { e = e0 + j; f = first; lo = s[j]; hi = s[j + 1]; }
+      first += n;
+    }
+    return make_int4(__builtin_amdgcn_readlane(e, src), __builtin_amdgcn_readlane(f, src),
+                     __builtin_amdgcn_readlane(lo, src), __builtin_amdgcn_readlane(hi, src));
   }
   // first M tile and number of M tiles of expert e
   __device__ __forceinline__ int2 tiles_of(int e, int BM, int incl) const {
-    const int n0 = (mid - lo + BM - 1) / BM, n1 = (hi - mid + BM - 1) / BM, first = incl - n0 - n1;
-    return make_int2(__builtin_amdgcn_readlane(e & 1 ? first + n0 : first, e >> 1),
-                     __builtin_amdgcn_readlane(e & 1 ? n1 : n0, e >> 1));
+    int first = first_tile(BM, incl), f = 0, c = 0;
+#pragma unroll
+    for (int j = 0; j < Q; ++j) {
+      const int n = tiles_at(j, BM);
+      if (e % Q == j) { f = first; c = n; }
+      first += n;
+    }
+    return make_int2(__builtin_amdgcn_readlane(f, e / Q), __builtin_amdgcn_readlane(c, e / Q));
   }
   // the rows of no expert: [0, x) and [y, R)
   __device__ __forceinline__ int2 covered() const {
-    return make_int2(__builtin_amdgcn_readlane(lo, 0),
-                     __builtin_amdgcn_readlane(E & 1 ? mid : hi, (E - 1) >> 1));
+    return make_int2(__builtin_amdgcn_readlane(s[0], 0), __builtin_amdgcn_readlane(s[Q], kWave - 1));
   }
 };
+
+// f(the scan), returned
+template <typename F>
+__device__ __forceinline__ auto with_scan(const int32_t* offsets, int E, int R, int lane, F&& f) {
+  if (E <= 2 * kWave) return f(OffsetScan<2>(offsets, E, R, lane));
+  return f(OffsetScan<16>(offsets, E, R, lane));
+}
 
 // zeroes the rows of no expert, by workgroup i of n with nt threads
 __device__ __forceinline__ void zero_rest(uint16_t* C, int64_t ldc, int N, int begin, int end, int R, int i, int n,
@@ -347,20 +376,24 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& P, int block, in
     int2 rg;
     if (P.split > 0) {
       // pieces of an expert's rows are laid out as the M tiles of a rows product are
-      const OffsetScan scan(P.offsets, P.E, P.R, lane);
-      int incl;
-      const int valid = scan.tiles(P.split, incl) * per;
-      if (block >= valid) return;
-      t = xcd_remap(block, valid);
-      e = __builtin_amdgcn_readfirstlane(t / per);       // the piece: C's index
-      const TileRec rec = scan.find(P.split, e, incl);
+      TileRec rec;
+      const bool mine = with_scan(P.offsets, P.E, P.R, lane, [&](const auto& scan) {
+        int incl;
+        const int valid = scan.tiles(P.split, incl) * per;
+        if (block >= valid) return false;
+        t = xcd_remap(block, valid);
+        e = __builtin_amdgcn_readfirstlane(t / per);     // the piece: C's index
+        rec = scan.find(P.split, e, incl);
+        return true;
+      });
+      if (!mine) return;
       rg.x = rec.z + (e - rec.y) * P.split;
       rg.y = min(rg.x + P.split, rec.w);
     } else {
       t = xcd_remap(block, nblocks);
       e = __builtin_amdgcn_readfirstlane(t / per);
       if (P.ranges != nullptr) rg = P.ranges[e];
-      else rg = OffsetScan(P.offsets, P.E, P.R, lane).rows(e);
+      else rg = with_scan(P.offsets, P.E, P.R, lane, [&](const auto& scan) { return scan.rows(e); });
     }
     int mt, nt;
     tile_order(t - e * per, P.mtiles, P.ntiles, 4, mt, nt);
@@ -374,26 +407,36 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& P, int block, in
     Bp = P.B + (int64_t)lo * P.ldb + n0;
     c_base = (int64_t)e * P.c_estride;
   } else {
-    int valid, t;
+    int valid, t, k0 = 0;
     TileRec rec;
+    if (P.ksplit > 1) {
+      nblocks /= P.ksplit;
+      const int piece = block / nblocks;
+      block -= piece * nblocks;
+      k0 = piece * P.klen;
+      c_base = piece * P.c_estride;
+    }
     if (P.tiles != nullptr) {
       valid = *P.n_mtiles * P.ntiles;
       if (block >= valid) return;
       t = xcd_remap(block, valid);
       rec = P.tiles[t / P.ntiles];
     } else {
-      const OffsetScan scan(P.offsets, P.E, P.R, lane);
-      const int grid = nblocks - P.rest_blocks;
-      if (block >= grid) {
-        const int2 c = scan.covered();
-        zero_rest(static_cast<uint16_t*>(P.C), P.ldc, P.N, c.x, c.y, P.R, block - grid, P.rest_blocks, NT);
-        return;
-      }
-      int incl;
-      valid = scan.tiles(BM, incl) * P.ntiles;
-      if (block >= valid) return;
-      t = xcd_remap(block, valid);
-      rec = scan.find(BM, t / P.ntiles, incl);
+      const bool mine = with_scan(P.offsets, P.E, P.R, lane, [&](const auto& scan) {
+        const int grid = nblocks - P.rest_blocks;
+        if (block >= grid) {
+          const int2 c = scan.covered();
+          zero_rest(static_cast<uint16_t*>(P.C), P.ldc, P.N, c.x, c.y, P.R, block - grid, P.rest_blocks, NT);
+          return false;
+        }
+        int incl;
+        valid = scan.tiles(BM, incl) * P.ntiles;
+        if (block >= valid) return false;
+        t = xcd_remap(block, valid);
+        rec = scan.find(BM, t / P.ntiles, incl);
+        return true;
+      });
+      if (!mine) return;
     }
     const int e = __builtin_amdgcn_readfirstlane(rec.x), first = __builtin_amdgcn_readfirstlane(rec.y);
     const int lo = __builtin_amdgcn_readfirstlane(rec.z), hi = __builtin_amdgcn_readfirstlane(rec.w);
@@ -402,9 +445,9 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& P, int block, in
     m0 = __builtin_amdgcn_readfirstlane(lo + mt * BM);
     n0 = __builtin_amdgcn_readfirstlane(nt * BN);
     mend = hi;
-    Kd = P.Kd;
-    Ap = P.A + (int64_t)m0 * P.lda;
-    Bp = P.B + (int64_t)e * P.b_estride + (BT ? (int64_t)n0 : (int64_t)n0 * P.ldb);
+    Kd = P.ksplit > 1 ? min(P.klen, P.Kd - k0) : P.Kd;
+    Ap = P.A + (int64_t)m0 * P.lda + k0;
+    Bp = P.B + (int64_t)e * P.b_estride + (BT ? (int64_t)k0 * P.ldb + n0 : (int64_t)n0 * P.ldb + k0);
   }
 
   // HQ: the tile's height in quarters of BM (an expert's short last tile; the

@@ -62,6 +62,8 @@ static void launch_form(const GroupedArgs& a, const GroupedPlan& plan, int64_t g
   const dim3 g((unsigned)grid);
   if (plan.bm == 256)
     hipLaunchKernelGGL((grouped_kernel<FORM, 256, 256, 2, 4, 2, OUT, 2, 3>), g, dim3(512), 0, st, a);
+  else if (plan.ksplit)
+    hipLaunchKernelGGL((grouped_kernel<FORM, 128, 128, 2, 2, 1, EPI_F32, 4, 4>), g, dim3(256), 0, st, a);
   else if (plan.deep)
     hipLaunchKernelGGL((grouped_kernel<FORM, 128, 128, 2, 2, 1, OUT, 4, 4>), g, dim3(256), 0, st, a);
   else
@@ -81,22 +83,75 @@ static void launch_form(const GroupedArgs& a, const GroupedPlan& plan, int64_t g
 // then ask for more than the L2 gives: 0.25 us of MFMA a k tile, 32 KB).
 constexpr int64_t kBigTiles = 192, kDeepGrid = 256;
 // Grids of at most this many workgroups find their tiles in the offsets
-// (OffsetScan, up to 128 experts) and need no table.
-constexpr int64_t kScanGrid = 1024;
+// (OffsetScan) and need no table; with more than 128 experts, 16 to a lane, of
+// at most the second number.
+constexpr int64_t kScanGrid = 1024, kScanGridWide = 512;
+// A rows product of few tiles and a long reduction (kSplitMinSteps k tiles) is
+// summed in pieces side by side, as many as give every CU a workgroup but of 4 k
+// tiles at least, and joined in order.
+constexpr int kSplitMinSteps = 24;
 
 static void finish_plan(GroupedPlan& p, int E) {
   p.deep = p.bm == 128 && p.grid <= kDeepGrid;
-  p.scan = p.grid <= kScanGrid && E <= kScanExperts;
+  p.scan = p.grid <= (E <= 2 * kWave ? kScanGrid : kScanGridWide);
 }
 
-GroupedPlan grouped_rows_plan(int64_t R, int E, int N) {
+GroupedPlan grouped_rows_plan(int64_t R, int E, int N, int kd, int kstep) {
   GroupedPlan p{};
   const int64_t big = (R / 256 + std::min<int64_t>(R, E) / 2) * ((N + 255) / 256);
   p.bm = R >= (int64_t)E * 128 && big >= kBigTiles ? 256 : 128;
   p.ntiles = (N + p.bm - 1) / p.bm;
   p.grid = grouped_max_tiles(R, E, p.bm) * p.ntiles;
   finish_plan(p, E);
+  const int steps = (kd + kstep - 1) / kstep;
+  const int unit = kstep == 64 ? 1 : kstep;             // (codes: pieces in whole blocks)
+  if (p.bm == 128 && p.grid > 0 && p.grid <= kDeepGrid / 2 && steps * kstep >= kSplitMinSteps * 64) {
+    const int pieces = (int)std::min<int64_t>(kDeepGrid / p.grid, std::max(2, steps / 4));
+    const int per = (steps + pieces - 1) / pieces;
+    p.ksplit = (steps + per - 1) / per;
+    p.klen = per * (kstep / unit);
+    if (p.ksplit < 2) p.ksplit = p.klen = 0;
+    else p.scan = true;
+  }
   return p;
+}
+
+size_t grouped_row_partial_bytes(const GroupedPlan& p, int64_t R, int N) {
+  return p.ksplit ? (size_t)p.ksplit * R * N * sizeof(float) : 0;
+}
+
+// A thread takes 8 columns of a row. Rows of no expert have no sums: zeros, or left as they are.
+__global__ void __launch_bounds__(256) rows_join_kernel(const float* __restrict__ partial, int pieces, int R, int N,
+                                                        const int32_t* __restrict__ offsets, int E, uint16_t* C,
+                                                        int64_t ldc, int rest) {
+  const int lane = threadIdx.x & 63;
+  const int2 c = with_scan(offsets, E, R, lane, [&](const auto& scan) { return scan.covered(); });
+  const int cpr = N / 8;
+  const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  if (i >= (int64_t)R * cpr) return;
+  const int r = (int)(i / cpr), n = (int)(i - (int64_t)r * cpr) * 8;
+  const bool own = r >= c.x && r < c.y;
+  if (!own && !rest) return;
+  f32x4 u{0.f, 0.f, 0.f, 0.f}, v = u;
+  if (own) {
+    const float* p = partial + (int64_t)r * N + n;
+    const int64_t step = (int64_t)R * N;
+#pragma unroll 4
+    for (int k = 0; k < pieces; ++k, p += step) {
+      u += *reinterpret_cast<const f32x4*>(p);
+      v += *reinterpret_cast<const f32x4*>(p + 4);
+    }
+  }
+  *reinterpret_cast<u32x4*>(C + (int64_t)r * ldc + n) =
+      u32x4{cvt_pk_bf16(u[0], u[1]), cvt_pk_bf16(u[2], u[3]), cvt_pk_bf16(v[0], v[1]), cvt_pk_bf16(v[2], v[3])};
+}
+
+hipError_t launch_rows_join(const float* partial, const GroupedPlan& plan, int64_t R, int N, const int32_t* offsets,
+                            int E, uint16_t* C, int64_t ldc, bool rest, hipStream_t st) {
+  const int64_t blocks = (R * (N / 8) + 255) / 256;
+  hipLaunchKernelGGL(rows_join_kernel, dim3((unsigned)blocks), dim3(256), 0, st, partial, plan.ksplit, (int)R, N,
+                     offsets, E, C, ldc, rest);
+  return hipGetLastError();
 }
 
 // A weight gradient of few tiles and many rows (less than half the CUs, 1024
@@ -110,7 +165,7 @@ GroupedPlan grouped_wgrad_plan(int64_t R, int E, int M, int N) {
   p.ntiles = (N + p.bm - 1) / p.bm;
   const int64_t tiles = (int64_t)p.mtiles * p.ntiles;
   p.grid = E * tiles;
-  if (p.bm == 128 && p.grid <= kDeepGrid / 2 && R >= 1024 && E <= kScanExperts) {
+  if (p.bm == 128 && p.grid <= kDeepGrid / 2 && R >= 1024) {
     const int64_t pieces = kDeepGrid / tiles;
     p.split = (int)std::max<int64_t>(256, (R + pieces - 1) / pieces + 63) / 64 * 64;
     p.pieces = grouped_max_tiles(R, E, p.split);
@@ -132,10 +187,11 @@ __global__ void __launch_bounds__(256) wgrad_join_kernel(const float* __restrict
                                                          int64_t size, int blocks) {
   const int lane = threadIdx.x & 63;
   const int e = blockIdx.x / blocks;
-  const OffsetScan scan(P.offsets, P.E, P.R, lane);
-  int incl;
-  scan.tiles(P.split, incl);
-  const int2 own = scan.tiles_of(e, P.split, incl);
+  const int2 own = with_scan(P.offsets, P.E, P.R, lane, [&](const auto& scan) {
+    int incl;
+    scan.tiles(P.split, incl);
+    return scan.tiles_of(e, P.split, incl);
+  });
   const int first = own.x, n = own.y;
   if (n == 0 && P.accumulate) return;
   const int64_t i = ((int64_t)(blockIdx.x - e * blocks) * 256 + threadIdx.x) * 4;
@@ -175,8 +231,15 @@ static GroupedArgs rows_args(const GroupedProduct& p, const GroupedPlan& plan, c
   a.offsets = p.offsets;
   a.E = p.E;
   a.R = (int)p.R;
-  a.rest_blocks = plan.scan && rest ? kScanRestBlocks : 0;
+  a.rest_blocks = plan.scan && rest && !plan.ksplit ? kScanRestBlocks : 0;
   a.ntiles = plan.ntiles;
+  if (plan.ksplit) {
+    a.C = s.row_partial;
+    a.ldc = p.N;
+    a.c_estride = p.R * p.N;
+    a.ksplit = plan.ksplit;
+    a.klen = plan.klen;
+  }
   return a;
 }
 
@@ -220,10 +283,12 @@ static hipError_t launch_join(const GroupedProduct& p, int M, bool f32, bool acc
 hipError_t launch_grouped_rows(const GroupedProduct& p, const GroupedPlan& plan, const GroupedScratch& s, bool rest,
                                hipStream_t st) {
   const GroupedArgs a = rows_args(p, plan, s, rest);
-  const int64_t grid = plan.grid + a.rest_blocks;
+  const int64_t grid = plan.grid * std::max(1, plan.ksplit) + a.rest_blocks;
   if (p.transposed_b) launch_form<FORM_NN, EPI_BF16>(a, plan, grid, st);
   else launch_form<FORM_NT, EPI_BF16>(a, plan, grid, st);
-  return hipGetLastError();
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !plan.ksplit) return e;
+  return launch_rows_join(s.row_partial, plan, p.R, p.N, p.offsets, p.E, static_cast<uint16_t*>(p.C), p.ldc, rest, st);
 }
 
 hipError_t launch_grouped_wgrad(const GroupedProduct& p, int M, bool f32, bool accumulate, const GroupedPlan& plan,
@@ -237,7 +302,7 @@ hipError_t launch_grouped_wgrad(const GroupedProduct& p, int M, bool f32, bool a
 }
 
 bool grouped_grad_in_one(const GroupedPlan& rows, const GroupedPlan& wgrad) {
-  return rows.bm == 128 && wgrad.bm == 128 && rows.scan && wgrad.scan;
+  return rows.bm == 128 && wgrad.bm == 128 && rows.scan && wgrad.scan && !rows.ksplit;
 }
 
 hipError_t launch_grouped_grad(const GroupedProduct& dx, const GroupedPlan& rows, bool rest, const GroupedProduct& dw,

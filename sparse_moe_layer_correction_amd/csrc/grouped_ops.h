@@ -10,7 +10,8 @@ struct GroupedScratch {
   int2* ranges;        // [E] rows of each expert
   int4* tiles;         // [grouped_max_tiles] M tile table
   int32_t* n_mtiles;   // [1]
-  float* partial;      // sums of the pieces of a split weight gradient
+  float* partial;      // sums of the pieces of a split weight gradient, or (after them) of a split rows product
+  float* row_partial;
 };
 
 // M tiles that R rows in E experts can need
@@ -31,15 +32,21 @@ struct GroupedProduct {
 struct GroupedPlan {
   int bm, mtiles, ntiles;
   int64_t grid;
+  int ksplit, klen;    // rows products: pieces of the reduction (0: none) and their length (codes: in blocks)
   int64_t pieces;      // split: the most pieces the rows can make
   int split;           // wgrad: rows of a piece, 0 for whole experts
   bool deep;           // four LDS stages
   bool scan;           // the kernel finds its tiles itself; else it needs launch_grouped_tiles
 };
 constexpr int kScanRestBlocks = 16;   // workgroups that zero the rows of no expert, without a table
-GroupedPlan grouped_rows_plan(int64_t R, int E, int N);
+// kd: the reduction's length; kstep: of a k tile (64, or 128 codes)
+GroupedPlan grouped_rows_plan(int64_t R, int E, int N, int kd, int kstep);
 GroupedPlan grouped_wgrad_plan(int64_t R, int E, int M, int N);
 size_t grouped_partial_bytes(const GroupedPlan& p, int M, int N);
+size_t grouped_row_partial_bytes(const GroupedPlan& p, int64_t R, int N);
+// C = the sum of a split rows product's pieces, over the rows of experts; rest: zero the others
+hipError_t launch_rows_join(const float* partial, const GroupedPlan& plan, int64_t R, int N, const int32_t* offsets,
+                            int E, uint16_t* C, int64_t ldc, bool rest, hipStream_t st);
 
 // Output whose rows of no expert are to be zeroed (C null: none).
 struct RestRows {
@@ -68,8 +75,10 @@ struct Fp8Args {
   const float* sx;             // [kb, R]
   const uint8_t* B;            // [E, N, K] codes of the weights
   const float* sw;             // [E, nb, kb]
-  uint16_t* C;
+  void* C;                     // bf16, or (a split reduction) the pieces' fp32 sums
   int64_t ldc, R;
+  int64_t c_stride;
+  int ksplit, klen;            // pieces of the reduction (0: none), their length in blocks of 128
   int N, K, nb, kb;
   const int4* tiles;           // null: found in the offsets
   const int32_t* n_mtiles;

@@ -45,18 +45,20 @@ int grouped_dims(const moe_grouped_dims* in, moe_grouped_dims* d) {
   if (d->E > kMaxExperts || d->R > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
   if ((d->N | d->K) % 8 || (d->ldx | d->ldy | d->ldw | d->w_stride | d->lddx) % 8) return MOE_ERR_UNSUPPORTED;
   if (std::max(std::max(d->ldx, d->ldy), std::max(d->ldw, d->lddx)) >= kMaxStride) return MOE_ERR_UNSUPPORTED;
-  for (int n : {d->N, d->K})
-    if (grouped_rows_plan(d->R, d->E, n).grid >= kMaxGrid) return MOE_ERR_UNSUPPORTED;
+  if (grouped_rows_plan(d->R, d->E, d->N, d->K, 64).grid >= kMaxGrid ||
+      grouped_rows_plan(d->R, d->E, d->K, d->N, 64).grid >= kMaxGrid)
+    return MOE_ERR_UNSUPPORTED;
   if (grouped_wgrad_plan(d->R, d->E, d->N, d->K).grid >= kMaxGrid) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
 
 // Workspace of a call: the tile table of the products that need one, and what the call adds.
 struct GroupedLayout {
-  size_t n_mtiles, ranges, tiles, partial, codes, scales, total;
+  size_t n_mtiles, ranges, tiles, partial, row_partial, codes, scales, total;
 };
 
-GroupedLayout grouped_layout(const moe_grouped_dims& d, int table_bm, size_t partial, bool quantise) {
+GroupedLayout grouped_layout(const moe_grouped_dims& d, int table_bm, size_t partial, size_t row_partial,
+                             bool quantise) {
   GroupedLayout l{};
   size_t o = 0;
   auto take = [&](size_t bytes) { const size_t at = o; o = align_up(o + bytes); return at; };
@@ -66,6 +68,7 @@ GroupedLayout grouped_layout(const moe_grouped_dims& d, int table_bm, size_t par
     l.tiles = take((size_t)grouped_max_tiles(d.R, d.E, table_bm) * 16);
   }
   if (partial > 0) l.partial = take(partial);
+  if (row_partial > 0) l.row_partial = take(row_partial);
   if (quantise) {
     l.codes = take((size_t)d.R * d.K);
     l.scales = take((size_t)((d.K + 127) / 128) * d.R * 4);
@@ -77,13 +80,14 @@ GroupedLayout grouped_layout(const moe_grouped_dims& d, int table_bm, size_t par
 GroupedScratch grouped_scratch(const GroupedLayout& l, void* ws) {
   char* p = static_cast<char*>(ws);
   return GroupedScratch{reinterpret_cast<int2*>(p + l.ranges), reinterpret_cast<int4*>(p + l.tiles),
-                        reinterpret_cast<int32_t*>(p + l.n_mtiles), reinterpret_cast<float*>(p + l.partial)};
+                        reinterpret_cast<int32_t*>(p + l.n_mtiles), reinterpret_cast<float*>(p + l.partial),
+                        reinterpret_cast<float*>(p + l.row_partial)};
 }
 
 int table_of(const GroupedPlan& p) { return p.scan ? 0 : p.bm; }
 
 GroupedLayout forward_layout(const moe_grouped_dims& d, const GroupedPlan& p, bool quantise = false) {
-  return grouped_layout(d, d.R > 0 ? table_of(p) : 0, 0, quantise);
+  return grouped_layout(d, d.R > 0 ? table_of(p) : 0, 0, grouped_row_partial_bytes(p, d.R, d.N), quantise);
 }
 
 struct GradPlans {
@@ -92,13 +96,14 @@ struct GradPlans {
 };
 
 GradPlans grad_plans(const moe_grouped_dims& d, bool dx, bool dw) {
-  GradPlans g{grouped_rows_plan(d.R, d.E, d.K), grouped_wgrad_plan(d.R, d.E, d.N, d.K), 0};
+  GradPlans g{grouped_rows_plan(d.R, d.E, d.K, d.N, 64), grouped_wgrad_plan(d.R, d.E, d.N, d.K), 0};
   if ((dx && !g.rows.scan) || (dw && !g.wgrad.scan)) g.table_bm = g.rows.bm;
   return g;
 }
 
-GroupedLayout grad_layout(const moe_grouped_dims& d, const GradPlans& g, bool dw) {
-  return grouped_layout(d, g.table_bm, dw ? grouped_partial_bytes(g.wgrad, d.N, d.K) : 0, false);
+GroupedLayout grad_layout(const moe_grouped_dims& d, const GradPlans& g, bool dx, bool dw) {
+  return grouped_layout(d, g.table_bm, dw ? grouped_partial_bytes(g.wgrad, d.N, d.K) : 0,
+                        dx ? grouped_row_partial_bytes(g.rows, d.R, d.K) : 0, false);
 }
 
 }  // namespace
@@ -109,9 +114,9 @@ size_t moe_grouped_workspace_bytes(const moe_grouped_dims* dims) {
   moe_grouped_dims d;
   if (grouped_dims(dims, &d) != MOE_OK) return 0;
   const GradPlans g = grad_plans(d, true, true);
-  const size_t q = d.K % 16 == 0 ? forward_layout(d, grouped_rows_plan(d.R, d.E, d.N), true).total : 0;
-  return std::max(std::max(forward_layout(d, grouped_rows_plan(d.R, d.E, d.N)).total, q),
-                  std::max(grad_layout(d, g, true).total, kAlign));
+  const size_t q = d.K % 16 == 0 ? forward_layout(d, grouped_rows_plan(d.R, d.E, d.N, d.K, 128), true).total : 0;
+  return std::max(std::max(forward_layout(d, grouped_rows_plan(d.R, d.E, d.N, d.K, 64)).total, q),
+                  std::max(grad_layout(d, g, true, true).total, kAlign));
 }
 
 int moe_grouped_matmul(const moe_grouped_dims* dims, const uint16_t* x, const uint16_t* w, const int32_t* offsets,
@@ -121,7 +126,7 @@ int moe_grouped_matmul(const moe_grouped_dims* dims, const uint16_t* x, const ui
   if (st != MOE_OK) return st;
   if (!w || !offsets || (d.R > 0 && (!x || !y))) return MOE_ERR_INVALID;
   if (!aligned16(x) || !aligned16(w) || !aligned16(y)) return MOE_ERR_INVALID;
-  const GroupedPlan plan = grouped_rows_plan(d.R, d.E, d.N);
+  const GroupedPlan plan = grouped_rows_plan(d.R, d.E, d.N, d.K, 64);
   const GroupedLayout l = forward_layout(d, plan);
   if (!ws_ok(ws, ws_bytes, l.total)) return MOE_ERR_WORKSPACE;
   if (d.R == 0) return MOE_OK;
@@ -146,7 +151,7 @@ int moe_grouped_matmul_grad(const moe_grouped_dims* dims, const uint16_t* dy, co
   const bool run_dx = dx && d.R > 0;
   const GradPlans plans = grad_plans(d, run_dx, dw != nullptr);
   const GroupedPlan &rows = plans.rows, &wg = plans.wgrad;
-  const GroupedLayout l = grad_layout(d, plans, dw != nullptr);
+  const GroupedLayout l = grad_layout(d, plans, run_dx, dw != nullptr);
   if (!ws_ok(ws, ws_bytes, l.total)) return MOE_ERR_WORKSPACE;
   const GroupedScratch s = grouped_scratch(l, ws);
   const RestRows rest{run_dx && !rows.scan && d.zero_rest ? dx : nullptr, d.lddx, d.K};
@@ -198,7 +203,7 @@ int fp8_impl(const moe_grouped_dims* dims, bool quantise, const uint16_t* x, con
   if (quantise && d.R >= kMaxBlocks / ((d.K + 127) / 128)) return MOE_ERR_UNSUPPORTED;
   if (!wq || !w_scale || !offsets || (d.R > 0 && (!y || (quantise ? !x : !xq || !xs)))) return MOE_ERR_INVALID;
   if (!aligned16(x) || !aligned16(xq) || !aligned16(wq) || !aligned16(y)) return MOE_ERR_INVALID;
-  const GroupedPlan plan = grouped_rows_plan(d.R, d.E, d.N);
+  const GroupedPlan plan = grouped_rows_plan(d.R, d.E, d.N, d.K, 128);
   const GroupedLayout l = forward_layout(d, plan, quantise);
   if (!ws_ok(ws, ws_bytes, l.total)) return MOE_ERR_WORKSPACE;
   if (d.R == 0) return MOE_OK;
@@ -229,9 +234,18 @@ int fp8_impl(const moe_grouped_dims* dims, bool quantise, const uint16_t* x, con
   a.n_mtiles = s.n_mtiles;
   a.offsets = offsets;
   a.E = d.E;
-  a.rest_blocks = plan.scan && d.zero_rest ? kScanRestBlocks : 0;
+  a.rest_blocks = plan.scan && d.zero_rest && !plan.ksplit ? kScanRestBlocks : 0;
   a.ntiles = plan.ntiles;
-  return hip_status(launch_grouped_fp8(a, plan, stream));
+  if (plan.ksplit) {
+    a.C = s.row_partial;
+    a.ldc = d.N;
+    a.c_stride = d.R * d.N;
+    a.ksplit = plan.ksplit;
+    a.klen = plan.klen;
+  }
+  if (launch_grouped_fp8(a, plan, stream) != hipSuccess) return MOE_ERR_HIP;
+  if (!plan.ksplit) return MOE_OK;
+  return hip_status(launch_rows_join(s.row_partial, plan, d.R, d.N, offsets, d.E, y, d.ldy, d.zero_rest != 0, stream));
 }
 
 }  // namespace

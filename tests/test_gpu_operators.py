@@ -125,6 +125,7 @@ def test_gradients_are_the_differences_of_the_product():
     assert abs(float(((yw - y) * dy.double()).sum()) - float((dw.double() * v.double()).sum())) <= slack
 
 
+@pytest.mark.parametrize("N,K", [(136, 72), (1800, 2064)])
 @pytest.mark.parametrize("raw", [
     [40, 60, 90, 150],          # rows before the first and behind the last expert
     [0, 120, 80, 200],          # descending: the second expert is empty, the third starts at 120
@@ -132,8 +133,9 @@ def test_gradients_are_the_differences_of_the_product():
     [200, 200, 200, 200],
     [0, 0, 0, 0],
 ])
-def test_rows_of_no_expert_and_bad_offsets(raw):
-    R, E, N, K = 200, 3, 136, 72
+def test_rows_of_no_expert_and_bad_offsets(raw, N, K):
+    """Short sums, and long ones that are split."""
+    R, E = 200, 3
     o = torch.tensor(raw, dtype=torch.int32).cuda()
     rg = ranges(o, R)
     own = torch.zeros(R, dtype=torch.bool)
@@ -327,8 +329,9 @@ def test_grouped_matmul_fp8(R, E, N, K, counts):
     assert torch.equal(y, M.grouped_matmul_fp8(codes, wq, sw, o, x_scale=scales))
 
 
-def test_fp8_rows_of_no_expert_and_special_values():
-    R, E, N, K = 300, 3, 136, 272
+@pytest.mark.parametrize("K", [272, 2064])
+def test_fp8_rows_of_no_expert_and_special_values(K):
+    R, E, N = 300, 3, 136
     o = torch.tensor([20, 150, 150, 280], dtype=torch.int32).cuda()
     x = rnd((R, K), 1)
     wq, sw = M.quantize_fp8_blocks(rnd((E, N, K), 2, K ** -0.5))
@@ -511,7 +514,7 @@ def test_other_streams():
         assert all(torch.equal(a, b) for a, b in zip(want, got))
 
 
-@pytest.mark.parametrize("R,E,N,K", [(300, 5, 136, 80), (1000, 200, 136, 80), (5000, 3, 136, 80)])
+@pytest.mark.parametrize("R,E,N,K", [(300, 5, 136, 80), (1000, 200, 520, 80), (5000, 3, 136, 80), (70, 3, 1600, 2064)])
 def test_workspace_of_the_caller(R, E, N, K):
     """Calls without a table, with one, and with the pieces of a split gradient, in a workspace full of junk."""
     x, w, dy = rnd((R, K), 1), rnd((E, N, K), 2), rnd((R, N), 3)
@@ -547,6 +550,10 @@ PLANS = [
     (1500, 1, 200, 336, [1500]),
     (40000, 2, 264, 144, [33000, 7000]),
     (30000, 7, 520, 2064, ragged(30000, 7, 4)),
+    (3, 14, 72, 5072, [0] * 4 + [1] + [0] * 5 + [2] + [0] * 3),
+    (538, 2, 1816, 3808, [500, 38]),
+    (900, 300, 72, 1552, ragged(900, 300, 5, 100)),
+    (400, 1024, 40, 80, ragged(400, 1024, 6, 700)),
 ]
 
 

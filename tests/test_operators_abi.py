@@ -54,7 +54,7 @@ def test_grouped_pointers(lib):
             a[i] = 264
             assert f(d, *a, 256, n, None) == -1
     assert f(None, 256, 256, 256, 256, 256, n, None) == -1
-    big = dims(E=200, R=10000)                     # needs a tile table
+    big = dims(E=200, R=10000, N=640)              # needs a tile table
     bn = lib.moe_grouped_workspace_bytes(big)
     for ws, have in ((None, bn), (128, bn), (256, 1024)):
         assert f(big, 256, 256, 256, 256, ws, have, None) == -3
@@ -63,7 +63,11 @@ def test_grouped_pointers(lib):
     # bf16 rows are quantised into the workspace
     assert lib.moe_grouped_matmul_fp8_rows(d, 256, 256, 256, 256, 256, 256, 100 * 128 - 1, None) == -3
     assert lib.moe_grouped_matmul_fp8_rows(d, 256, 256, 256, 256, 256, None, 0, None) == -3
-    # a weight gradient split over the rows keeps its pieces there
+    # a long reduction over few tiles keeps its pieces there
+    assert f(dims(K=4096), 256, 256, 256, 256, None, 0, None) == -3
+    assert q(dims(K=4096), *[256] * 6, None, 0, None) == -3
+    assert g(dims(N=4096), 256, 256, 256, 256, 256, None, 0, 0, None, 0, None) == -3
+    # and so does a weight gradient split over the rows
     assert g(dims(R=4096, E=1), 256, 256, 256, 256, None, 256, 0, 0, None, 0, None) == -3
     assert g(d, None, 256, 256, 256, 256, 256, 0, 0, 256, n, None) == -1
     assert g(d, 256, None, 256, 256, 256, 256, 0, 0, 256, n, None) == -1      # dw needs x
