@@ -78,10 +78,15 @@ static void launch_form(const GroupedArgs& a, const GroupedPlan& plan, int64_t g
 //   wgrad, R 8000, E 30, [504, 3000] (720 big tiles)         59 / 81 / 104
 //   wgrad, R 20000, E 2, [640, 640] (18 big, 50 small)        - / 100 / 62
 //   dgrad, R 2000, E 16, [1200, 400] (124 small tiles)        - / 15.8 / 13.2
-// So the big tile where its tiles come near the 256 CUs' number, else the small
-// one, with four stages while every workgroup has a CU to itself (more of them
-// then ask for more than the L2 gives: 0.25 us of MFMA a k tile, 32 KB).
-constexpr int64_t kBigTiles = 192, kDeepGrid = 256;
+//   rows product, R 17097, E 12, [368, 4952] (144 big tiles)  91 / 98 / 104
+//   wgrad, R 76894, E 329, [112, 560] (half of a big tile)    44 / 33 / -
+// So the big tile where its tiles are more than half the 256 CUs' number and
+// compute little beyond the output's edge (kBigPadding times the small tiles'),
+// else the small one, with four stages while every workgroup has a CU to itself
+// (more of them then ask for more than the L2 gives: 0.25 us of MFMA a k tile, 32 KB).
+constexpr int64_t kBigTiles = 136, kDeepGrid = 256;
+constexpr double kBigPadding = 1.3;
+static int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 // Grids of at most this many workgroups find their tiles in the offsets
 // (OffsetScan) and need no table; with more than 128 experts, 16 to a lane, of
 // at most the second number.
@@ -99,7 +104,8 @@ static void finish_plan(GroupedPlan& p, int E) {
 GroupedPlan grouped_rows_plan(int64_t R, int E, int N, int kd, int kstep) {
   GroupedPlan p{};
   const int64_t big = (R / 256 + std::min<int64_t>(R, E) / 2) * ((N + 255) / 256);
-  p.bm = R >= (int64_t)E * 128 && big >= kBigTiles ? 256 : 128;
+  const bool fits = up(N, 256) <= kBigPadding * up(N, 128);
+  p.bm = R >= (int64_t)E * 128 && big >= kBigTiles && fits ? 256 : 128;
   p.ntiles = (N + p.bm - 1) / p.bm;
   p.grid = grouped_max_tiles(R, E, p.bm) * p.ntiles;
   finish_plan(p, E);
@@ -160,7 +166,8 @@ hipError_t launch_rows_join(const float* partial, const GroupedPlan& plan, int64
 // 20000 rows 62 us in one piece each. Pieces are multiples of a k tile, 256 rows or more.
 GroupedPlan grouped_wgrad_plan(int64_t R, int E, int M, int N) {
   GroupedPlan p{};
-  p.bm = (int64_t)E * ((M + 255) / 256) * ((N + 255) / 256) >= kBigTiles ? 256 : 128;
+  const bool fits = up(M, 256) * up(N, 256) <= kBigPadding * up(M, 128) * up(N, 128);
+  p.bm = (int64_t)E * ((M + 255) / 256) * ((N + 255) / 256) >= kBigTiles && fits ? 256 : 128;
   p.mtiles = (M + p.bm - 1) / p.bm;
   p.ntiles = (N + p.bm - 1) / p.bm;
   const int64_t tiles = (int64_t)p.mtiles * p.ntiles;
