@@ -624,18 +624,20 @@ def _need_matrix(t, name):
 _ERR_WORKSPACE = -3
 
 
-def _grouped_call(fn, d: _GroupedDims, index, ws, *args):
+def _grouped_call(fn, d: _GroupedDims, index, ws, *args, needs_ws: bool = False):
     """fn(d, *args, ws, ws_bytes, stream) on GPU `index`'s current stream. Without a caller's
-    workspace the first try has none, which small calls do not need; the others refuse
-    before any launch and get one."""
+    workspace the first try has none, which small calls do not need (but for `needs_ws`);
+    the others refuse before any launch and get one."""
     torch = _torch()
     dr = ctypes.byref(d)
     # (torch.cuda.current_stream wraps the same handle in a Stream object: 2 us a call)
     stream = torch._C._cuda_getCurrentRawStream(index)
     if ws is None:
-        rc = fn(dr, *args, None, 0, stream)
+        rc = _ERR_WORKSPACE if needs_ws else fn(dr, *args, None, 0, stream)
         if rc == _ERR_WORKSPACE:
             nbytes = load_library().moe_grouped_workspace_bytes(dr)
+            if nbytes == 0:              # refused dims: the call says which
+                _check(fn(dr, *args, None, 0, stream))
             ws = torch.empty(nbytes, dtype=torch.uint8, device=torch.device("cuda", index))
             rc = fn(dr, *args, ws.data_ptr(), nbytes, stream)
     else:
@@ -784,7 +786,11 @@ def grouped_matmul_fp8(x, w_codes, w_scale, offsets, *, x_scale=None, out=None, 
     kb, nb = (K + 127) // 128, (N + 127) // 128
     if not w_codes.is_contiguous():
         raise ValueError("w_codes must be contiguous")
-    _need(w_scale, "w_scale", torch.float32, (E, nb, kb), dev)
+    if not isinstance(w_scale, torch.Tensor) or w_scale.dtype is not torch.float32:
+        raise TypeError("w_scale must be an fp32 torch tensor")
+    if w_scale.shape != (E, nb, kb) or not w_scale.is_contiguous() or w_scale.get_device() != index:
+        raise ValueError(f"w_scale must be contiguous of shape {(E, nb, kb)} on GPU {index}, got "
+                         f"{tuple(w_scale.shape)} on {w_scale.device}")
     ldx = 0
     if x_scale is None:
         ldx = _need_rows(x, "x", torch.bfloat16, R, K, index)
@@ -801,7 +807,7 @@ def grouped_matmul_fp8(x, w_codes, w_scale, offsets, *, x_scale=None, out=None, 
     d = _GroupedDims(R, E, N, K, ldx, ldy, 0, 0, 0, fresh)
     if x_scale is None:
         _grouped_call(lib.moe_grouped_matmul_fp8_rows, d, index, ws, x.data_ptr(), w_codes.data_ptr(),
-                      w_scale.data_ptr(), offsets.data_ptr(), out.data_ptr())
+                      w_scale.data_ptr(), offsets.data_ptr(), out.data_ptr(), needs_ws=R > 0)
     else:
         _grouped_call(lib.moe_grouped_matmul_fp8, d, index, ws, x.data_ptr(), x_scale.data_ptr(), w_codes.data_ptr(),
                       w_scale.data_ptr(), offsets.data_ptr(), out.data_ptr())
@@ -842,7 +848,7 @@ def _grad_table(grads, outs):
         raise ValueError("grads must hold at least one tensor")
     every = grads if outs is None else grads + outs
     index = grads[0].get_device() if isinstance(grads[0], T) else -1
-    if index < 0 or not all(isinstance(t, T) for t in every):
+    if index < 0 or not all(issubclass(k, T) for k in set(map(type, every))):
         _refuse_grads(grads, grads if outs is None else outs, index)
     kinds = [t.dtype for t in every]
     sizes = list(map(T.numel, every))
@@ -851,13 +857,13 @@ def _grad_table(grads, outs):
             or (outs is not None and (kinds[:n] != kinds[n:] or sizes[:n] != sizes[n:])):
         _refuse_grads(grads, grads if outs is None else outs, index)
     # four 64-bit words an entry: grad, out, n, dtype (and its padding)
-    at = array("q", map(T.data_ptr, every))
+    at = array("q", list(map(T.data_ptr, every)))
     raw = array("q", bytes(32 * n))
     raw[0::4] = at[:n]
     if outs is not None:
         raw[1::4] = at[n:]
     raw[2::4] = array("q", sizes[:n])
-    raw[3::4] = array("q", [k is torch.float32 for k in kinds[:n]])
+    raw[3::4] = array("q", list(map({torch.bfloat16: 0, torch.float32: 1}.__getitem__, kinds[:n])))
     return ctypes.cast(raw.buffer_info()[0], ctypes.POINTER(_GradTensor)), raw, n, grads[0]
 
 
