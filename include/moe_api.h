@@ -328,7 +328,7 @@ int moe_forward_noalloc(const moe_dims* dims, const moe_weights* w, const uint16
  * below the weight's extent), null or not 16-byte aligned tensors.
  * MOE_ERR_UNSUPPORTED: N, K or a stride not a multiple of 8 (the kernels move 16
  * bytes per lane; K a multiple of 16 for the 8-bit product), E > 1024,
- * R >= 2^31, a row stride >= 2^22, a product of 2^23 tiles (of 128 x 128 or
+ * R > 2^30, a row stride >= 2^21, a product of 2^23 tiles (of 128 x 128 or
  * more) or more.
  * Outputs may not overlap inputs. R = 0 is valid (its row tensors may be null). */
 typedef struct moe_grouped_dims {

@@ -42,12 +42,24 @@ __global__ void __launch_bounds__(1024) grouped_tiles_kernel(const int32_t* __re
   __syncthreads();
   int first = it - nt;
   for (int w = 0; w < wave; ++w) first += wsum[w];
-  if (tid < E) {
-    ranges[tid] = make_int2(lo, hi);
-    if (tiles != nullptr)
-      for (int i = 0; i < nt; ++i) tiles[first + i] = make_int4(tid, first, lo, hi);
-  }
+  if (tid < E) ranges[tid] = make_int2(lo, hi);
   if (tid == E - 1) *n_mtiles = first + nt;
+  // the records, a thread for every 1024th of them (an expert with all rows has
+  // thousands): the last expert that starts at or before the tile, empty ones
+  // starting where the next one does
+  __shared__ int starts[1024], from[1024], to[1024], total;
+  starts[tid] = tid < E ? first : 0x7FFFFFFF;
+  from[tid] = lo;
+  to[tid] = hi;
+  if (tid == E - 1) total = first + nt;
+  __syncthreads();
+  for (int i = tid; i < total; i += 1024) {
+    int e = 0;
+#pragma unroll
+    for (int d = 512; d >= 1; d >>= 1)
+      if (e + d < 1024 && starts[e + d] <= i) e += d;
+    tiles[i] = make_int4(e, starts[e], from[e], to[e]);
+  }
 }
 
 hipError_t launch_grouped_tiles(const int32_t* offsets, int E, int R, int BM, const GroupedScratch& s,

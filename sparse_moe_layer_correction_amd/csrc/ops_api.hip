@@ -26,7 +26,8 @@ bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 
 // a grid's threads are counted in 32 bits; workgroups have up to 512
 constexpr int64_t kMaxGrid = (int64_t)1 << 23;
 constexpr int64_t kMaxBlocks = (int64_t)1 << 28;   // 16 to a workgroup of 256 threads
-constexpr int64_t kMaxStride = (int64_t)1 << 22;   // 256 rows of 2 bytes stay below 2 GiB
+constexpr int64_t kMaxStride = (int64_t)1 << 21;   // 256 rows of 2 bytes and their k offsets stay below 2 GiB
+constexpr int64_t kMaxRows = (int64_t)1 << 30;     // row counts round up to whole tiles in 32 bits
 
 // dims with the dense strides filled in
 int grouped_dims(const moe_grouped_dims* in, moe_grouped_dims* d) {
@@ -42,7 +43,7 @@ int grouped_dims(const moe_grouped_dims* in, moe_grouped_dims* d) {
   if (d->w_stride == 0) d->w_stride = (int64_t)d->N * d->ldw;
   if (d->ldx < d->K || d->ldy < d->N || d->ldw < d->K || d->lddx < d->K || d->w_stride < extent)
     return MOE_ERR_INVALID;
-  if (d->E > kMaxExperts || d->R > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
+  if (d->E > kMaxExperts || d->R > kMaxRows) return MOE_ERR_UNSUPPORTED;
   if ((d->N | d->K) % 8 || (d->ldx | d->ldy | d->ldw | d->w_stride | d->lddx) % 8) return MOE_ERR_UNSUPPORTED;
   if (std::max(std::max(d->ldx, d->ldy), std::max(d->ldw, d->lddx)) >= kMaxStride) return MOE_ERR_UNSUPPORTED;
   if (grouped_rows_plan(d->R, d->E, d->N, d->K, 64).grid >= kMaxGrid ||

@@ -193,6 +193,46 @@ def test_strided_operands():
         check(dw[e], G.t() @ Z, G.abs().t() @ Z.abs(), b - a, BF)
 
 
+def test_refused_on_the_gpu():
+    """Layouts the kernels cannot read, refused by the binding or the library before any launch."""
+    x, w, o, dy = rnd((16, 64), 1), rnd((2, 72, 64), 2), offs([8, 8]), rnd((16, 72), 3)
+    bad = [
+        lambda: M.grouped_matmul(x[:1].expand(16, 64), w, o),               # rows that share memory
+        lambda: M.grouped_matmul(x, w[:1].expand(2, 72, 64), o),            # experts that share theirs
+        lambda: M.grouped_matmul(x.t().contiguous().t(), w, o),             # columns not contiguous
+        lambda: M.grouped_matmul(x, w, o.long()),
+        lambda: M.grouped_matmul(x, w, o[:-1]),
+        lambda: M.grouped_matmul(x.float(), w, o),
+        lambda: M.grouped_matmul(x[:, :56], w, o),
+        lambda: M.grouped_matmul(x, w, o, out=torch.empty(16, 64, dtype=BF, device="cuda")),
+        lambda: M.grouped_matmul(x, w, o.cpu()),
+        lambda: M.grouped_matmul(rnd((16, 65), 1)[:, :64], w, o),           # a row stride that is no multiple of 8
+        lambda: M.grouped_matmul(rnd((16, 72), 1)[:, 4:68], w, o),          # not 16-byte aligned
+        lambda: M.grouped_matmul(x[:, :60], w[:, :, :60], o),               # K no multiple of 8
+        lambda: M.grouped_matmul_grad(dy, x, w, o, need_dx=False, need_dw=False),
+        lambda: M.grouped_matmul_grad(dy, x, w, o, accumulate=True),
+        lambda: M.grouped_matmul_grad(dy, x, w, o, dw_dtype=torch.float16),
+        lambda: M.grouped_matmul_grad(dy, x, w, o, dw=torch.empty(2, 72, 64, device="cuda"), dw_dtype=BF),
+        lambda: M.grouped_matmul_grad(x, x, w, o),
+        lambda: M.grouped_matmul_fp8(x, w, torch.ones(2, 1, 1, device="cuda"), o),
+        lambda: M.grouped_matmul_fp8(x, w.view(torch.uint8)[..., :64].contiguous(), torch.ones(2, 1, 2, device="cuda"), o),
+        lambda: M.quantize_fp8_rows(x.float()),
+        lambda: M.quantize_fp8_blocks(w.transpose(1, 2)),
+        lambda: M.clip_grad_norm([x, x], 1.0),                              # twice the same: scaled twice
+        lambda: M.clip_grad_norm([x, x[8:]], 1.0),
+        lambda: M.clip_grad_norm([x], 1.0, out=[]),
+        lambda: M.clip_grad_norm([x], 1.0, out=[x.float()]),
+        lambda: M.clip_grad_norm([x.t()], 1.0),
+        lambda: M.clip_grad_norm([x], -1.0),
+        lambda: M.grad_norm([x, o]),
+        lambda: M.grad_norm([x, x.cpu()]),
+    ]
+    for f in bad:
+        with pytest.raises((TypeError, ValueError, M.MoEError)):
+            f()
+    assert float(M.grad_norm([x, x])) > 0                                   # the norm alone may count a tensor twice
+
+
 def test_no_rows():
     E, N, K = 4, 64, 72
     x, w, o = torch.empty(0, K, dtype=BF, device="cuda"), rnd((E, N, K), 1), offs([0] * E)
@@ -554,6 +594,9 @@ PLANS = [
     (538, 2, 1816, 3808, [500, 38]),
     (900, 300, 72, 1552, ragged(900, 300, 5, 100)),
     (400, 1024, 40, 80, ragged(400, 1024, 6, 700)),
+    (2000, 200, 1032, 80, ragged(2000, 200, 7, 60)),
+    (60000, 150, 1032, 64, ragged(60000, 150, 8, 20)),
+    (30000, 2, 136, 64, [29999, 1]),
 ]
 
 
@@ -582,6 +625,10 @@ def test_every_plan(R, E, N, K, counts):
         ref, s = ops(XV[a:b], wv.t().contiguous())
         loss = 7 * 2.0 ** -13 * (XV[a:b].abs().view(b - a, K // 8, 8).amax(2) @ wv.abs().view(N, K // 8, 8).amax(2).t())
         check(y8[a:b], ref, s, K + 2 * ((K + 127) // 128), BF, loss.cpu())
-    keep = dw.clone()
+    # added to itself: fp32 sums double exactly, bf16 ones too (the sum, once rounded, plus the same fp32 sum
+    # is within a step of twice it)
+    keep, keepb = dw.clone(), dwb.clone()
     M.grouped_matmul_grad(dy, x, w, o, need_dx=False, dw=dw, accumulate=True)
-    assert torch.allclose(dw, 2 * keep, rtol=2.0 ** -22, atol=0)
+    M.grouped_matmul_grad(dy, x, w, o, need_dx=False, dw=dwb, accumulate=True)
+    assert torch.equal(dw, 2 * keep)
+    assert ((dwb.double() - 2 * keepb.double()).abs() <= 2.0 ** -7 * 2 * keepb.double().abs()).all()

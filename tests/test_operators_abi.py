@@ -27,8 +27,8 @@ REFUSED = [
     (dict(ldx=120), -1), (dict(ldy=56), -1), (dict(ldw=64), -1), (dict(lddx=64), -1), (dict(w_stride=64 * 128 - 8), -1),
     (dict(ldx=-128), -1),
     (dict(N=60), -2), (dict(K=100), -2), (dict(ldx=132), -2), (dict(w_stride=64 * 128 + 4), -2),
-    (dict(E=1025), -2), (dict(R=1 << 31), -2), (dict(ldx=1 << 22), -2),
-    (dict(R=(1 << 31) - 1, N=1 << 20), -2), (dict(E=1024, N=1 << 15, K=1 << 15), -2),
+    (dict(E=1025), -2), (dict(R=(1 << 30) + 1), -2), (dict(ldx=1 << 21), -2),
+    (dict(R=1 << 30, N=1 << 20), -2), (dict(E=1024, N=1 << 15, K=1 << 15), -2),
 ]
 
 
@@ -87,7 +87,7 @@ def test_grouped_pointers(lib):
         a[i] = None
         assert r(d, *a, 256, n, None) == -1
     assert r(dims(ldx=120), *[256] * 5, 256, n, None) == -1
-    assert r(dims(R=(1 << 31) - 1, K=4096), *[256] * 5, 256, 1 << 50, None) == -2
+    assert r(dims(R=1 << 30, K=4096), *[256] * 5, 256, 1 << 50, None) == -2
 
 
 def test_quantisers(lib):
