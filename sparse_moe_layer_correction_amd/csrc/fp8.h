@@ -41,8 +41,10 @@ grouped_fp8_kernel(const Fp8Args P) {
   static_assert(128 % WTN == 0, "a wave's columns lie in one weight block");
   // (the halves of the row stages are arrays of their own: the compiler waits for
   // every load into an array before it reads from it)
-  __shared__ u32x4 sa0[BM * 4], sa0h[BM * 4], sb0[BN * 8], sa1[BM * 4], sa1h[BM * 4], sb1[BN * 8];
-  __shared__ float sc0[BM], sc1[BM];
+  constexpr int AH = BM * 8 / NT > 1 ? BM * 4 : BM * 8;   // chunks of a row stage's array: half, or all of it
+  constexpr int AHH = BM * 8 / NT > 1 ? BM * 4 : 1;
+  __shared__ u32x4 sa0[AH], sa0h[AHH], sb0[BN * 8], sa1[AH], sa1h[AHH], sb1[BN * 8];
+  __shared__ float sc0[BM < 64 ? 64 : BM], sc1[BM < 64 ? 64 : BM];
 
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -95,8 +97,8 @@ grouped_fp8_kernel(const Fp8Args P) {
     constexpr int HQ = decltype(height)::value;
     constexpr int H = BM * HQ / 4, WTM = H / WM, TM = WTM / 16;
     static_assert(TM >= 2 && TM % 2 == 0 && H * 8 % NT == 0, "wave tile");
-    // (a quarter tile's rows are one load a thread: they go whole, at the second barrier)
-    constexpr bool HALVES = HQ != 1;
+    // (few rows are one load a thread: they go whole, at the second barrier)
+    constexpr bool HALVES = H * 8 / NT > 1;
     constexpr int HR = HALVES ? H / 2 : H;            // rows of a row stage array
     typedef OperandLoad<HR, false, NT, HALVES ? WTM / 2 : 0> LoadA;
     constexpr int NA = LoadA::NL, NB = BN * 8 / NT;
@@ -110,7 +112,7 @@ grouped_fp8_kernel(const Fp8Args P) {
 
     // a k tile's row scales: one dword per lane, 64 rows a wave (waves beyond
     // the tile's rows repeat others'); rows past the end repeat the last one
-    constexpr int SW = H / 64;
+    constexpr int SW = H < 64 ? 1 : H / 64;
     const int srow = (wave % SW) * 64;
     const uint32_t sofs = (uint32_t)min(srow + lane, hi - 1 - m0) * 4;
     auto issue_scales = [&](float* st, int kt) {
@@ -255,8 +257,8 @@ grouped_fp8_kernel(const Fp8Args P) {
     }
     // through LDS to whole rows of the wave tile, as store_wave_tile
     constexpr int CPW = WTN / 8, RPI = 64 / CPW, NRB = WTM / RPI, SB = WTM * WTN * 2;
-    constexpr int APER = BM * 64 / SB, BPER = BN * 128 / SB;     // wave tiles in a row half, in a weight stage
-    static_assert(APER >= 1 && WM * WN <= 4 * APER + 2 * BPER, "staging areas");
+    constexpr int APER = std::max(1, AH * 16 / SB), BPER = BN * 128 / SB;   // wave tiles in a row array, in a weight stage
+    static_assert(WM * WN <= 2 * BPER || (AH * 16 >= SB && WM * WN <= 4 * APER + 2 * BPER), "staging areas");
     u32x4* const area = wave < BPER                 ? sb0
                         : wave < 2 * BPER            ? sb1
                         : wave < 2 * BPER + APER     ? sa0

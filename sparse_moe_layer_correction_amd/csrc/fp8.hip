@@ -143,7 +143,11 @@ hipError_t launch_fp8_blocks(const uint16_t* w, int64_t count, int N, int K, uin
 
 hipError_t launch_grouped_fp8(const Fp8Args& a, const GroupedPlan& plan, hipStream_t st) {
   const dim3 grid((unsigned)(plan.grid * std::max(1, plan.ksplit)) + a.rest_blocks);
-  if (plan.ksplit)
+  if (plan.bm == 32 && plan.ksplit)
+    hipLaunchKernelGGL((grouped_fp8_kernel<32, 128, 1, 4, 4, EPI_F32>), grid, dim3(256), 0, st, a);
+  else if (plan.bm == 32)
+    hipLaunchKernelGGL((grouped_fp8_kernel<32, 128, 1, 4, 4, EPI_BF16>), grid, dim3(256), 0, st, a);
+  else if (plan.ksplit)
     hipLaunchKernelGGL((grouped_fp8_kernel<128, 128, 2, 2, 2, EPI_F32>), grid, dim3(256), 0, st, a);
   else if (plan.bm == 256)
     hipLaunchKernelGGL((grouped_fp8_kernel<256, 256, 2, 4, 2, EPI_BF16>), grid, dim3(512), 0, st, a);

@@ -619,13 +619,18 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& P, int block, in
     }
     MOE_WAIT_VMCNT(0);   // no load may write a stage that the epilogue uses, or that the next workgroup gets
     __syncthreads();
-    // 16 KB of staging per wave: an array each, or half of one
-    constexpr int per = BM * 8 * 16 / 16384;
-    static_assert(WM * WN <= 4 * per, "staging areas");
-    const int h = wave / per;
-    char* stg = reinterpret_cast<char*>(h == 0 ? sa0 : h == 1 ? sb0 : h == 2 ? sa1 : sb1) + (wave % per) * 16384;
+    // staging: all of it in one array, or 16 KB a wave in an array each or half of one
+    constexpr int ES = OUT == EPI_F32 ? 4 : 2, SB = WTM * WTN * ES;
+    char* stg;
+    if constexpr (WM * WN * SB <= BN * 128) {
+      stg = reinterpret_cast<char*>(sb0) + wave * SB;
+    } else {
+      constexpr int per = BM * 8 * 16 / 16384;
+      static_assert(WM * WN <= 4 * per, "staging areas");
+      const int h = wave / per;
+      stg = reinterpret_cast<char*>(h == 0 ? sa0 : h == 1 ? sb0 : h == 2 ? sa1 : sb1) + (wave % per) * 16384;
+    }
     const int mw = m0 + wave_m * WTM, nw = n0 + wave_n * WTN;
-    constexpr int ES = OUT == EPI_F32 ? 4 : 2;
     void* dst = static_cast<char*>(P.C) + (c_base + (int64_t)mw * P.ldc + nw) * ES;
     bool add = false;
     if constexpr (FORM == FORM_TN) {

@@ -72,6 +72,15 @@ hipError_t launch_grouped_tiles(const int32_t* offsets, int E, int R, int BM, co
 template <int FORM, int OUT>
 static void launch_form(const GroupedArgs& a, const GroupedPlan& plan, int64_t grid, hipStream_t st) {
   const dim3 g((unsigned)grid);
+  if constexpr (FORM != FORM_TN) {
+    if (plan.bm == 32) {
+      if (plan.ksplit)
+        hipLaunchKernelGGL((grouped_kernel<FORM, 32, 128, 1, 4, 2, EPI_F32, 4, 4>), g, dim3(256), 0, st, a);
+      else
+        hipLaunchKernelGGL((grouped_kernel<FORM, 32, 128, 1, 4, 2, OUT, 4, 4>), g, dim3(256), 0, st, a);
+      return;
+    }
+  }
   if (plan.bm == 256)
     hipLaunchKernelGGL((grouped_kernel<FORM, 256, 256, 2, 4, 2, OUT, 2, 3>), g, dim3(512), 0, st, a);
   else if (plan.ksplit)
@@ -98,6 +107,9 @@ static void launch_form(const GroupedArgs& a, const GroupedPlan& plan, int64_t g
 // (more of them then ask for more than the L2 gives: 0.25 us of MFMA a k tile, 32 KB).
 constexpr int64_t kBigTiles = 136, kDeepGrid = 256;
 constexpr double kBigPadding = 1.3;
+#ifndef FEWR
+#define FEWR 24
+#endif
 static int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 // Grids of at most this many workgroups find their tiles in the offsets
 // (OffsetScan) and need no table; with more than 128 experts, 16 to a lane, of
@@ -113,17 +125,18 @@ static void finish_plan(GroupedPlan& p, int E) {
   p.scan = p.grid <= (E <= 2 * kWave ? kScanGrid : kScanGridWide);
 }
 
-GroupedPlan grouped_rows_plan(int64_t R, int E, int N, int kd, int kstep) {
+GroupedPlan grouped_rows_plan(int64_t R, int E, int N, int kd, int kstep, bool few) {
   GroupedPlan p{};
   const int64_t big = (R / 256 + std::min<int64_t>(R, E) / 2) * ((N + 255) / 256);
   const bool fits = up(N, 256) <= kBigPadding * up(N, 128);
-  p.bm = R >= (int64_t)E * 128 && big >= kBigTiles && fits ? 256 : 128;
-  p.ntiles = (N + p.bm - 1) / p.bm;
+  p.bm = R >= (int64_t)E * 128 && big >= kBigTiles && fits ? 256 : few && R < (int64_t)E * FEWR ? 32 : 128;
+  const int bn = std::max(p.bm, 128);
+  p.ntiles = (N + bn - 1) / bn;
   p.grid = grouped_max_tiles(R, E, p.bm) * p.ntiles;
   finish_plan(p, E);
   const int steps = (kd + kstep - 1) / kstep;
   const int unit = kstep == 64 ? 1 : kstep;             // (codes: pieces in whole blocks)
-  if (p.bm == 128 && p.grid > 0 && p.grid <= kDeepGrid / 2 && steps * kstep >= kSplitMinSteps * 64) {
+  if (p.bm <= 128 && p.grid > 0 && p.grid <= kDeepGrid / 2 && steps * kstep >= kSplitMinSteps * 64) {
     const int pieces = (int)std::min<int64_t>(kDeepGrid / p.grid, std::max(2, steps / 4));
     const int per = (steps + pieces - 1) / pieces;
     p.ksplit = (steps + per - 1) / per;

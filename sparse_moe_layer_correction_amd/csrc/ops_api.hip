@@ -97,7 +97,9 @@ struct GradPlans {
 };
 
 GradPlans grad_plans(const moe_grouped_dims& d, bool dx, bool dw) {
-  GradPlans g{grouped_rows_plan(d.R, d.E, d.K, d.N, 64), grouped_wgrad_plan(d.R, d.E, d.N, d.K), 0};
+  GradPlans g{grouped_rows_plan(d.R, d.E, d.K, d.N, 64, false), grouped_wgrad_plan(d.R, d.E, d.N, d.K), 0};
+  // (dx by itself may take the tile for few rows; in one launch with dw both have the same)
+  if (!dx || !dw || !grouped_grad_in_one(g.rows, g.wgrad)) g.rows = grouped_rows_plan(d.R, d.E, d.K, d.N, 64);
   if ((dx && !g.rows.scan) || (dw && !g.wgrad.scan)) g.table_bm = g.rows.bm;
   return g;
 }

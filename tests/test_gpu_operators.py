@@ -597,6 +597,8 @@ PLANS = [
     (2000, 200, 1032, 80, ragged(2000, 200, 7, 60)),
     (60000, 150, 1032, 64, ragged(60000, 150, 8, 20)),
     (30000, 2, 136, 64, [29999, 1]),
+    (1000, 100, 520, 1040, ragged(1000, 100, 9, 40)),
+    (300, 100, 72, 2064, [33, 0, 64, 32, 31, 1] + [2] * 69 + [1] + [0] * 24),
 ]
 
 
