@@ -107,9 +107,13 @@ static void launch_form(const GroupedArgs& a, const GroupedPlan& plan, int64_t g
 // (more of them then ask for more than the L2 gives: 0.25 us of MFMA a k tile, 32 KB).
 constexpr int64_t kBigTiles = 136, kDeepGrid = 256;
 constexpr double kBigPadding = 1.3;
-#ifndef FEWR
-#define FEWR 24
-#endif
+// Few rows to an expert (fewer than this many on average): the weights' bytes
+// bound the product, and what counts is how many of them are on their way. Tiles
+// of 32 rows with four stages, two workgroups to a CU, have 96 KB of weights in
+// flight a CU, 128-row tiles of two stages 32. us, 128-row / 32-row tiles, E 100,
+// [1024, 2048]: 20 rows 104 / 96 (dgrad 97 / 87), 40 rows 91 / 92 (102 / 106), 80
+// rows 115 / 126 (115 / 124); codes 43 / 39, 45 / 41, 49 / 49.
+constexpr int kFewRows = 24, kFewRowsCodes = 48;
 static int64_t up(int64_t v, int64_t m) { return (v + m - 1) / m * m; }
 // Grids of at most this many workgroups find their tiles in the offsets
 // (OffsetScan) and need no table; with more than 128 experts, 16 to a lane, of
@@ -129,7 +133,8 @@ GroupedPlan grouped_rows_plan(int64_t R, int E, int N, int kd, int kstep, bool f
   GroupedPlan p{};
   const int64_t big = (R / 256 + std::min<int64_t>(R, E) / 2) * ((N + 255) / 256);
   const bool fits = up(N, 256) <= kBigPadding * up(N, 128);
-  p.bm = R >= (int64_t)E * 128 && big >= kBigTiles && fits ? 256 : few && R < (int64_t)E * FEWR ? 32 : 128;
+  const int64_t few_rows = (int64_t)E * (kstep == 64 ? kFewRows : kFewRowsCodes);
+  p.bm = R >= (int64_t)E * 128 && big >= kBigTiles && fits ? 256 : few && R < few_rows ? 32 : 128;
   const int bn = std::max(p.bm, 128);
   p.ntiles = (N + bn - 1) / bn;
   p.grid = grouped_max_tiles(R, E, p.bm) * p.ntiles;
