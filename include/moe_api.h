@@ -328,9 +328,10 @@ int moe_forward_noalloc(const moe_dims* dims, const moe_weights* w, const uint16
  * below the weight's extent), null or not 16-byte aligned tensors.
  * MOE_ERR_UNSUPPORTED: N, K or a stride not a multiple of 8 (the kernels move 16
  * bytes per lane; K a multiple of 16 for the 8-bit product), E > 1024,
- * R > 2^30, a row stride >= 2^21, a product of 2^23 tiles (of 128 x 128 or
+ * R > 2^30, a row stride >= 2^21, a product of 2^23 tiles (of 32 x 128 or
  * more) or more.
- * Outputs may not overlap inputs. R = 0 is valid (its row tensors may be null). */
+ * Outputs may not share memory with inputs or each other (MOE_ERR_INVALID; columns
+ * side by side in one matrix, with one row stride, do not). R = 0 is valid (its row tensors may be null). */
 typedef struct moe_grouped_dims {
   int64_t R;
   int32_t E, N, K;
@@ -375,7 +376,7 @@ int moe_grouped_matmul_grad(const moe_grouped_dims* dims, const uint16_t* dy, co
  *   blocks: w [count, N, K] bf16 dense, blocks of 128 x 128:
  *           codes [count, N, K], scales [count, ceil(N/128), ceil(K/128)]
  * MOE_ERR_INVALID: R, count < 0, N, K <= 0, ldx < K, null or not 16-byte aligned
- * x, w, codes; MOE_ERR_UNSUPPORTED: K or ldx not a multiple of 8, 2^28 blocks of
+ * x, w, codes, memory shared between them; MOE_ERR_UNSUPPORTED: K or ldx not a multiple of 8, 2^28 blocks of
  * rows or 2^24 blocks of weights or more, N * K >= 2^31. */
 int moe_quantize_fp8_rows(const uint16_t* x, int64_t R, int32_t K, int64_t ldx, uint8_t* codes, float* scales,
                           hipStream_t stream);
@@ -416,7 +417,7 @@ typedef struct moe_grad_tensor {
  * `tensors` is read during the call only. Nothing waits for the GPU.
  * MOE_ERR_INVALID: count < 0, null tensors with count > 0, a null, misaligned or
  * negative-length tensor, an unknown dtype, max_norm negative or NaN, a null
- * norm, or (clip) outputs that overlap each other or another gradient.
+ * norm, or (clip) outputs, the norm among them, that overlap each other or another gradient.
  * MOE_ERR_UNSUPPORTED: more than 2^40 elements. ws: 256-byte aligned. */
 size_t moe_grad_norm_workspace_bytes(const moe_grad_tensor* tensors, int32_t count);
 int moe_grad_norm(const moe_grad_tensor* tensors, int32_t count, float* norm, void* ws, size_t ws_bytes,

@@ -4,6 +4,7 @@
 #include "../../include/moe_api.h"
 
 #include <algorithm>
+#include <initializer_list>
 #include <new>
 #include <utility>
 #include <vector>
@@ -47,11 +48,44 @@ int grouped_dims(const moe_grouped_dims* in, moe_grouped_dims* d) {
   if ((d->N | d->K) % 8 || (d->ldx | d->ldy | d->ldw | d->w_stride | d->lddx) % 8) return MOE_ERR_UNSUPPORTED;
   if (std::max(std::max(d->ldx, d->ldy), std::max(d->ldw, d->lddx)) >= kMaxStride) return MOE_ERR_UNSUPPORTED;
   if (grouped_rows_plan(d->R, d->E, d->N, d->K, 64).grid >= kMaxGrid ||
+      grouped_rows_plan(d->R, d->E, d->N, d->K, 128).grid >= kMaxGrid ||
       grouped_rows_plan(d->R, d->E, d->K, d->N, 64).grid >= kMaxGrid)
     return MOE_ERR_UNSUPPORTED;
   if (grouped_wgrad_plan(d->R, d->E, d->N, d->K).grid >= kMaxGrid) return MOE_ERR_UNSUPPORTED;
   return MOE_OK;
 }
+
+// Memory of a tensor: `rows` rows of `width` bytes, `pitch` apart.
+struct Region {
+  const void* p;
+  int64_t rows, width, pitch;
+};
+
+// Whether two regions share memory (columns side by side in one matrix do not).
+bool overlap(const Region& a, const Region& b) {
+  if (!a.p || !b.p || a.rows <= 0 || b.rows <= 0) return false;
+  const uintptr_t al = reinterpret_cast<uintptr_t>(a.p), bl = reinterpret_cast<uintptr_t>(b.p);
+  const uintptr_t ah = al + (uintptr_t)((a.rows - 1) * a.pitch + a.width);
+  const uintptr_t bh = bl + (uintptr_t)((b.rows - 1) * b.pitch + b.width);
+  if (ah <= bl || bh <= al) return false;
+  if (a.pitch != b.pitch) return true;
+  const bool a_first = al <= bl;
+  const int64_t at = (int64_t)((a_first ? bl - al : al - bl) % (uintptr_t)a.pitch);
+  return at < (a_first ? a.width : b.width) || at + (a_first ? b.width : a.width) > a.pitch;
+}
+bool overlaps_any(const Region& out, std::initializer_list<Region> others) {
+  for (const Region& o : others)
+    if (overlap(out, o)) return true;
+  return false;
+}
+Region rows_region(const void* p, int64_t R, int64_t cols, int64_t ld, int bytes) {
+  return Region{p, R, cols * bytes, ld * bytes};
+}
+Region dense_region(const void* p, int64_t bytes) { return Region{p, 1, bytes, bytes}; }
+Region weight_region(const void* w, const moe_grouped_dims& d) {
+  return dense_region(w, ((d.E - 1) * d.w_stride + (int64_t)(d.N - 1) * d.ldw + d.K) * 2);
+}
+Region offsets_region(const int32_t* o, const moe_grouped_dims& d) { return dense_region(o, (int64_t)(d.E + 1) * 4); }
 
 // Workspace of a call: the tile table of the products that need one, and what the call adds.
 struct GroupedLayout {
@@ -116,10 +150,11 @@ extern "C" {
 size_t moe_grouped_workspace_bytes(const moe_grouped_dims* dims) {
   moe_grouped_dims d;
   if (grouped_dims(dims, &d) != MOE_OK) return 0;
-  const GradPlans g = grad_plans(d, true, true);
+  size_t grad = kAlign;
+  for (int outs = 1; outs <= 3; ++outs)                 // dx, dw, both: their plans differ
+    grad = std::max(grad, grad_layout(d, grad_plans(d, outs & 1, outs & 2), outs & 1, outs & 2).total);
   const size_t q = d.K % 16 == 0 ? forward_layout(d, grouped_rows_plan(d.R, d.E, d.N, d.K, 128), true).total : 0;
-  return std::max(std::max(forward_layout(d, grouped_rows_plan(d.R, d.E, d.N, d.K, 64)).total, q),
-                  std::max(grad_layout(d, g, true, true).total, kAlign));
+  return std::max(std::max(forward_layout(d, grouped_rows_plan(d.R, d.E, d.N, d.K, 64)).total, q), grad);
 }
 
 int moe_grouped_matmul(const moe_grouped_dims* dims, const uint16_t* x, const uint16_t* w, const int32_t* offsets,
@@ -132,6 +167,9 @@ int moe_grouped_matmul(const moe_grouped_dims* dims, const uint16_t* x, const ui
   const GroupedPlan plan = grouped_rows_plan(d.R, d.E, d.N, d.K, 64);
   const GroupedLayout l = forward_layout(d, plan);
   if (!ws_ok(ws, ws_bytes, l.total)) return MOE_ERR_WORKSPACE;
+  if (overlaps_any(rows_region(y, d.R, d.N, d.ldy, 2),
+                   {rows_region(x, d.R, d.K, d.ldx, 2), weight_region(w, d), offsets_region(offsets, d)}))
+    return MOE_ERR_INVALID;
   if (d.R == 0) return MOE_OK;
   const GroupedScratch s = grouped_scratch(l, ws);
   const RestRows rest{d.zero_rest ? y : nullptr, d.ldy, d.N};
@@ -156,6 +194,11 @@ int moe_grouped_matmul_grad(const moe_grouped_dims* dims, const uint16_t* dy, co
   const GroupedPlan &rows = plans.rows, &wg = plans.wgrad;
   const GroupedLayout l = grad_layout(d, plans, run_dx, dw != nullptr);
   if (!ws_ok(ws, ws_bytes, l.total)) return MOE_ERR_WORKSPACE;
+  const Region rdy = rows_region(dy, d.R, d.N, d.ldy, 2), rx = rows_region(dw ? x : nullptr, d.R, d.K, d.ldx, 2);
+  const Region rw = weight_region(run_dx ? w : nullptr, d), ro = offsets_region(offsets, d);
+  const Region rdx = rows_region(run_dx ? dx : nullptr, d.R, d.K, d.lddx, 2);
+  const Region rdw = dense_region(dw, (int64_t)d.E * d.N * d.K * (dw_dtype == MOE_FP32 ? 4 : 2));
+  if (overlaps_any(rdx, {rdy, rx, rw, ro, rdw}) || overlaps_any(rdw, {rdy, rx, rw, ro})) return MOE_ERR_INVALID;
   const GroupedScratch s = grouped_scratch(l, ws);
   const RestRows rest{run_dx && !rows.scan && d.zero_rest ? dx : nullptr, d.lddx, d.K};
   if (plans.table_bm > 0)
@@ -176,6 +219,9 @@ int moe_quantize_fp8_rows(const uint16_t* x, int64_t R, int32_t K, int64_t ldx, 
   if (ldx == 0) ldx = K;
   if (ldx < K || (R > 0 && (!x || !codes || !scales)) || !aligned16(x) || !aligned16(codes)) return MOE_ERR_INVALID;
   if (K % 8 || ldx % 8 || R >= kMaxBlocks / ((K + 127) / 128)) return MOE_ERR_UNSUPPORTED;
+  const Region rq = dense_region(codes, R * K), rs = dense_region(scales, R * ((K + 127) / 128) * 4);
+  const Region rx = rows_region(x, R, K, ldx, 2);
+  if (R > 0 && (overlap(rx, rq) || overlap(rx, rs) || overlap(rq, rs))) return MOE_ERR_INVALID;
   return hip_status(launch_fp8_rows(x, R, K, ldx, codes, scales, stream));
 }
 
@@ -185,6 +231,10 @@ int moe_quantize_fp8_blocks(const uint16_t* w, int64_t count, int32_t N, int32_t
   if ((count > 0 && (!w || !codes || !scales)) || !aligned16(w) || !aligned16(codes)) return MOE_ERR_INVALID;
   if (K % 8 || (int64_t)N * K > 0x7FFFFFFF) return MOE_ERR_UNSUPPORTED;
   if (count >= (kMaxGrid * 2) / ((int64_t)((N + 127) / 128) * ((K + 127) / 128))) return MOE_ERR_UNSUPPORTED;
+  const int64_t n = count * N * K;
+  const Region rq = dense_region(codes, n), rw = dense_region(w, n * 2);
+  const Region rs = dense_region(scales, count * ((N + 127) / 128) * ((K + 127) / 128) * 4);
+  if (count > 0 && (overlap(rw, rq) || overlap(rw, rs) || overlap(rq, rs))) return MOE_ERR_INVALID;
   return hip_status(launch_fp8_blocks(w, count, N, K, codes, scales, stream));
 }
 
@@ -209,6 +259,12 @@ int fp8_impl(const moe_grouped_dims* dims, bool quantise, const uint16_t* x, con
   const GroupedPlan plan = grouped_rows_plan(d.R, d.E, d.N, d.K, 128);
   const GroupedLayout l = forward_layout(d, plan, quantise);
   if (!ws_ok(ws, ws_bytes, l.total)) return MOE_ERR_WORKSPACE;
+  const int64_t kb = (d.K + 127) / 128, nb = (d.N + 127) / 128;
+  if (overlaps_any(rows_region(y, d.R, d.N, d.ldy, 2),
+                   {rows_region(x, d.R, d.K, d.ldx, 2), dense_region(xq, d.R * d.K), dense_region(xs, kb * d.R * 4),
+                    dense_region(wq, (int64_t)d.E * d.N * d.K), dense_region(w_scale, d.E * nb * kb * 4),
+                    offsets_region(offsets, d)}))
+    return MOE_ERR_INVALID;
   if (d.R == 0) return MOE_OK;
   const GroupedScratch s = grouped_scratch(l, ws);
   if (quantise) {
@@ -231,8 +287,8 @@ int fp8_impl(const moe_grouped_dims* dims, bool quantise, const uint16_t* x, con
   a.R = d.R;
   a.N = d.N;
   a.K = d.K;
-  a.nb = (d.N + 127) / 128;
-  a.kb = (d.K + 127) / 128;
+  a.nb = (int)nb;
+  a.kb = (int)kb;
   a.tiles = plan.scan ? nullptr : s.tiles;
   a.n_mtiles = s.n_mtiles;
   a.offsets = offsets;
@@ -391,17 +447,19 @@ int norm_impl(const moe_grad_tensor* t, int32_t count, double max_norm, float* n
   });
 }
 
-// Outputs that overlap each other, or a gradient that is not the output's own.
-bool outputs_overlap(const moe_grad_tensor* t, int32_t count) {
-  struct Span { uintptr_t lo, hi; int32_t i; bool out; };
+// Outputs (the norm is one) that overlap each other, or a gradient that is not the output's own.
+bool outputs_overlap(const moe_grad_tensor* t, int32_t count, const float* norm) {
+  struct Span { uintptr_t lo, hi; bool out; };
   std::vector<Span> v;
-  v.reserve(2 * (size_t)count);
+  v.reserve(2 * (size_t)count + 1);
+  const uintptr_t at = reinterpret_cast<uintptr_t>(norm);
+  if (norm) v.push_back({at, at + sizeof(float), true});
   for (int32_t i = 0; i < count; ++i) {
     if (t[i].n == 0) continue;
     const uintptr_t g = reinterpret_cast<uintptr_t>(t[i].grad), o = t[i].out ? reinterpret_cast<uintptr_t>(t[i].out) : g;
     const uintptr_t b = (uintptr_t)t[i].n * dtype_size(t[i].dtype);
-    v.push_back({o, o + b, i, true});
-    if (o != g) v.push_back({g, g + b, i, false});
+    v.push_back({o, o + b, true});
+    if (o != g) v.push_back({g, g + b, false});
   }
   std::sort(v.begin(), v.end(), [](const Span& a, const Span& b) { return a.lo < b.lo; });
   // sweep: the furthest end so far of outputs and of gradients
@@ -436,7 +494,7 @@ int moe_clip_grad_norm(const moe_grad_tensor* tensors, int32_t count, float max_
   if (st != MOE_OK) return st;
   if (!(max_norm >= 0.f)) return MOE_ERR_INVALID;
   try {
-    if (outputs_overlap(tensors, count)) return MOE_ERR_INVALID;
+    if (outputs_overlap(tensors, count, norm)) return MOE_ERR_INVALID;
   } catch (const std::bad_alloc&) {
     return MOE_ERR_WORKSPACE;
   }

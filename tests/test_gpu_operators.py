@@ -193,6 +193,52 @@ def test_strided_operands():
         check(dw[e], G.t() @ Z, G.abs().t() @ Z.abs(), b - a, BF)
 
 
+def test_columns_of_one_matrix():
+    """Operands side by side in one matrix share its rows and no memory."""
+    R, E, N, K = 150, 3, 136, 72
+    both, w, o = torch.zeros(R, K + N, dtype=BF, device="cuda"), rnd((E, N, K), 2, K ** -0.5), offs([60, 0, 90])
+    both[:, :K] = rnd((R, K), 1)
+    x = both[:, :K].clone()
+    y = M.grouped_matmul(x, w, o)
+    assert M.grouped_matmul(both[:, :K], w, o, out=both[:, K:]).data_ptr() == both.data_ptr() + 2 * K
+    assert torch.equal(both[:, K:], y) and torch.equal(both[:, :K], x)
+
+
+@pytest.mark.parametrize("R,E,N,K", [(1100, 50, 64, 2048), (1100, 50, 2048, 64)])
+def test_each_gradient_alone(R, E, N, K):
+    """Alone, each gradient may take other tiles, and another workspace, than both together."""
+    x, w, dy, o = rnd((R, K), 1), rnd((E, N, K), 2, K ** -0.5), rnd((R, N), 3), offs(ragged(R, E, 4, 5))
+    dx = M.grouped_matmul_grad(dy, x, w, o, need_dw=False)[0]
+    dw = M.grouped_matmul_grad(dy, x, w, o, need_dx=False, dw_dtype=F32)[1]
+    for e, (a, b) in enumerate(ranges(o, R)):
+        G, X, Wt = dy[a:b].double(), x[a:b].double(), w[e].double()
+        check(dw[e], (G.t() @ X).cpu(), (G.abs().t() @ X.abs()).cpu(), b - a, F32)
+        if b > a:
+            check(dx[a:b], (G @ Wt).cpu(), (G.abs() @ Wt.abs()).cpu(), N, BF)
+
+
+@pytest.mark.parametrize("tail", [3, 300])
+def test_rows_past_32_bit_offsets(tail):
+    """Rows of 8 KB, 600000 of them: byte offsets past 2^32 in x, y and dy, and the last rows still right."""
+    R, E, N, K = 600000 + tail, 3, 4096, 64
+    o = offs([599990, 0, R - 599990])
+    x, w, dy = rnd((R, K), 1), rnd((E, N, K), 2, K ** -0.5), rnd((R, 1), 3).expand(R, N).contiguous()
+    y = M.grouped_matmul(x, w, o)
+    dx, dw = M.grouped_matmul_grad(dy, x, w, o, dw_dtype=F32)
+    G, X, Wt = dy[599990:].double(), x[599990:].double(), w[2].double()
+    check(y[599990:], (X @ Wt.t().contiguous()).cpu(), (X.abs() @ Wt.abs().t().contiguous()).cpu(), K, BF)
+    check(dx[599990:], (G @ Wt).cpu(), (G.abs() @ Wt.abs()).cpu(), N, BF)
+    check(dw[2], (G.t() @ X).cpu(), (G.abs().t() @ X.abs()).cpu(), R - 599990, F32)
+    xt = dy[-tail:].clone()                                                 # and as the operand read along its rows
+    wt = rnd((E, 72, N), 4, N ** -0.5)
+    z = M.grouped_matmul(dy, wt, o)
+    check(z[-tail:], (xt.double() @ wt[2].double().t().contiguous()).cpu(),
+          (xt.double().abs() @ wt[2].double().abs().t().contiguous()).cpu(), N, BF)
+    q, s = M.quantize_fp8_rows(dy)
+    q2, s2 = M.quantize_fp8_rows(xt)
+    assert torch.equal(q[-tail:], q2) and torch.equal(s[:, -tail:], s2)
+
+
 def test_refused_on_the_gpu():
     """Layouts the kernels cannot read, refused by the binding or the library before any launch."""
     x, w, o, dy = rnd((16, 64), 1), rnd((2, 72, 64), 2), offs([8, 8]), rnd((16, 72), 3)
@@ -226,6 +272,12 @@ def test_refused_on_the_gpu():
         lambda: M.clip_grad_norm([x], -1.0),
         lambda: M.grad_norm([x, o]),
         lambda: M.grad_norm([x, x.cpu()]),
+    ]
+    sq = rnd((2, 64, 64), 4)
+    bad += [
+        lambda: M.grouped_matmul(x, sq, o, out=x),                          # an output over an input
+        lambda: M.grouped_matmul_grad(x, x, sq, o, dx=x),
+        lambda: M.grouped_matmul_grad(x, x.clone(), sq, o, dw=sq),
     ]
     for f in bad:
         with pytest.raises((TypeError, ValueError, M.MoEError)):

@@ -1,6 +1,7 @@
 """The expert operators' argument checks, before any launch: no GPU needed."""
 import ctypes
 import os
+import random
 
 import pytest
 import torch
@@ -29,6 +30,7 @@ REFUSED = [
     (dict(N=60), -2), (dict(K=100), -2), (dict(ldx=132), -2), (dict(w_stride=64 * 128 + 4), -2),
     (dict(E=1025), -2), (dict(R=(1 << 30) + 1), -2), (dict(ldx=1 << 21), -2),
     (dict(R=1 << 30, N=1 << 20), -2), (dict(E=1024, N=1 << 15, K=1 << 15), -2),
+    (dict(R=47 * 1024, E=1024, N=425984, K=16), -2),           # too many 32-row tiles, of the 8-bit product alone
 ]
 
 
@@ -109,6 +111,49 @@ def test_quantisers(lib):
     assert b(256, 1 << 24, 8, 8, 256, 256, None) == -2
 
 
+def test_outputs_share_no_memory(lib):
+    R, N, K = 100, 64, 128
+    d, f, g = dims(), lib.moe_grouped_matmul, lib.moe_grouped_matmul_grad
+    x, w, o, y, dx, dw, ws = (i << 24 for i in range(1, 8))
+    for out in (x, x + R * K * 2 - 16, x - R * N * 2 + 16, w, w + 4 * N * K * 2 - 16, o, o + 16):
+        assert f(d, x, w, o, out, None, 0, None) == -1, hex(out)
+    n = lib.moe_grouped_workspace_bytes(d)
+    for a, b in ((y, dw), (x, dw), (w, dw), (dw, dw), (o, dw), (dx, x), (dx, y), (dx, dx + 16), (dx, o)):
+        assert g(d, y, x, w, o, a, b, 1, 0, ws, n, None) == -1, (hex(a), hex(b))
+    # columns of one matrix that overlap: x in [0, 128), y in [120, 184) of rows of 256
+    side = dims(ldx=256, ldy=256)
+    assert f(side, x, w, o, x + 120 * 2, None, 0, None) == -1
+    assert f(side, x + 120 * 2, w, o, x + 64 * 2, None, 0, None) == -1
+    assert f(side, x, w, o, x + 200 * 2, None, 0, None) == -1          # ends in the next row's x
+    xq, xs, wq, sw = (i << 24 for i in range(10, 14))
+    for out in (xq, xs, wq, sw, o, xq + R * K - 16):
+        assert lib.moe_grouped_matmul_fp8(d, xq, xs, wq, sw, o, out, None, 0, None) == -1, hex(out)
+    assert lib.moe_grouped_matmul_fp8_rows(d, x, wq, sw, o, x, ws, n, None) == -1
+    assert lib.moe_quantize_fp8_rows(x, R, K, 0, x, xs, None) == -1
+    assert lib.moe_quantize_fp8_rows(x, R, K, 0, xq, xq + 64, None) == -1
+    assert lib.moe_quantize_fp8_blocks(w, 4, N, K, wq, w + 64, None) == -1
+
+
+def test_workspace_is_enough_for_every_call(lib):
+    """Given moe_grouped_workspace_bytes, no call asks for more: those below share memory between an input and an
+    output, and are refused for that (-1), after the workspace (-3)."""
+    rng = random.Random(7)
+    x, w, o, y, ws = (i << 40 for i in range(1, 6))
+    cases = [(1100, 50, 64, 2048)] + [
+        (int(2 ** rng.uniform(0, 15)), int(2 ** rng.uniform(0, 10)), 16 * rng.randint(1, 200), 16 * rng.randint(1, 200))
+        for _ in range(2000)]
+    for R, E, N, K in cases:
+        d = ctypes.byref(M._GroupedDims(R, E, N, K))
+        n = lib.moe_grouped_workspace_bytes(d)
+        got = (lib.moe_grouped_matmul(d, x, w, o, x, ws, n, None),
+               lib.moe_grouped_matmul_grad(d, y, x, w, o, y, None, 1, 0, ws, n, None),
+               lib.moe_grouped_matmul_grad(d, y, x, w, o, None, x, 1, 0, ws, n, None),
+               lib.moe_grouped_matmul_grad(d, y, x, w, o, y, x, 0, 0, ws, n, None),
+               lib.moe_grouped_matmul_fp8(d, x, y, w, w, o, x, ws, n, None),
+               lib.moe_grouped_matmul_fp8_rows(d, x, w, w, o, x, ws, n, None))
+        assert set(got) == {-1}, (R, E, N, K, got)
+
+
 def tensors(*spec):
     t = (M._GradTensor * max(1, len(spec)))()
     for e, (g, o, n, dt) in zip(t, spec):
@@ -149,7 +194,9 @@ def test_clip_refuses_overlaps(lib):
         [(256, 8192, 1000, 1), (512, 260, 10, 1)],              # inside a longer one
     ):
         t = tensors(*spec)
-        assert c(t, len(spec), 1.0, 256, 256, 1 << 20, None) == -1, spec
+        assert c(t, len(spec), 1.0, 1 << 30, 256, 1 << 20, None) == -1, spec
+    for norm in (256, 256 + 396, 4096 + 200):                   # the norm's own place inside a gradient or an output
+        assert c(tensors((256, 4096, 100, 1)), 1, 1.0, norm, 256, 1 << 20, None) == -1, norm
 
 
 def test_binding_refuses():
