@@ -352,6 +352,20 @@ struct GroupedLds {
   __shared__ u32x4 sa2[AST == 4 ? BM * 8 : 1], sa3[AST == 4 ? BM * 8 : 1], sb3[AST == 4 ? BN * 8 : 1]; \
   const GroupedLds lds{sa0, sa1, sa2, sa3, sb0, sb1, sb2, sb3}
 
+// Tile of workgroup `block` of a weight gradient: runs of g tiles go to the XCDs
+// in turn (xcd_remap's one run an XCD shares more rows in an L2, but experts
+// differ in length, and the XCD with the longest ones ends the launch alone).
+// us, dx and fp32 dW, one run / runs of 8 / of 16 tiles: R 65536 over 64 experts as
+// 1/rank^1.1, [2048, 2048] 1711 / 1144 / 1245, R 16384 over 8, [2048, 1024] 205 /
+// 146 / 185; even, R 65536 1171 / 1182 / 1172, R 32768 over 128, [2048, 5120] 2360 /
+// 2307 / 2334.
+constexpr int kWgradRun = 8;
+__device__ __forceinline__ int xcd_runs(int block, int nblocks, int g) {
+  if (block >= nblocks / (8 * g) * (8 * g)) return block;
+  const int x = block % 8, j = block / 8;
+  return (j / g * 8 + x) * g + j % g;
+}
+
 // Workgroup `block` of the `nblocks` of one product: a C tile BM x BN by WM x WN
 // waves. OUT: EPI_BF16 or EPI_F32.
 template <int FORM, int BM, int BN, int WM, int WN, int OUT, int AST, int BST>
@@ -390,7 +404,7 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& P, int block, in
       rg.x = rec.z + (e - rec.y) * P.split;
       rg.y = min(rg.x + P.split, rec.w);
     } else {
-      t = xcd_remap(block, nblocks);
+      t = xcd_runs(block, nblocks, min(per, kWgradRun));
       e = __builtin_amdgcn_readfirstlane(t / per);
       if (P.ranges != nullptr) rg = P.ranges[e];
       else rg = with_scan(P.offsets, P.E, P.R, lane, [&](const auto& scan) { return scan.rows(e); });
@@ -677,16 +691,18 @@ grouped_kernel(const GroupedArgs P) {
   grouped_body<FORM, BM, BN, WM, WN, OUT, AST, BST>(P, blockIdx.x, gridDim.x, lds);
 }
 
-// Both gradients in one launch: the first g0 workgroups take dx, the others dW
-// (independent sums that leave CUs idle when each runs alone).
+// Both gradients in one launch: the first g0 workgroups take dW, the others dx.
+// The two are independent, and what one leaves idle the other fills: the CUs
+// beside a long expert's dW, whose tiles start first, and those of dx's last
+// tiles.
 template <int BM, int BN, int WM, int WN, int OCC, int OUT, int AST, int BST>
 __global__ void __launch_bounds__(64 * WM * WN, 1) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
 grouped_grad_kernel(const GroupedArgs DX, const GroupedArgs DW, int g0) {
   MOE_GROUPED_LDS(BM, BN, AST, BST);
   if ((int)blockIdx.x < g0)
-    grouped_body<FORM_NN, BM, BN, WM, WN, EPI_BF16, AST, BST>(DX, blockIdx.x, g0, lds);
+    grouped_body<FORM_TN, BM, BN, WM, WN, OUT, AST, BST>(DW, blockIdx.x, g0, lds);
   else
-    grouped_body<FORM_TN, BM, BN, WM, WN, OUT, AST, BST>(DW, (int)blockIdx.x - g0, (int)gridDim.x - g0, lds);
+    grouped_body<FORM_NN, BM, BN, WM, WN, EPI_BF16, AST, BST>(DX, (int)blockIdx.x - g0, (int)gridDim.x - g0, lds);
 }
 
 }  // namespace moe

@@ -339,6 +339,7 @@ hipError_t launch_grouped_wgrad(const GroupedProduct& p, int M, bool f32, bool a
 }
 
 bool grouped_grad_in_one(const GroupedPlan& rows, const GroupedPlan& wgrad) {
+  if (rows.bm == 256 && wgrad.bm == 256) return true;
   return rows.bm == 128 && wgrad.bm == 128 && rows.scan && wgrad.scan && !rows.ksplit;
 }
 
@@ -346,10 +347,14 @@ hipError_t launch_grouped_grad(const GroupedProduct& dx, const GroupedPlan& rows
                                const GroupedPlan& wgrad, int M, bool f32, bool accumulate, const GroupedScratch& s,
                                hipStream_t st) {
   const GroupedArgs a = rows_args(dx, rows, s, rest), b = wgrad_args(dw, M, accumulate, wgrad, s);
-  const int g0 = (int)rows.grid + a.rest_blocks;
-  const dim3 grid((unsigned)(g0 + wgrad.grid));
+  const int g0 = (int)wgrad.grid;
+  const dim3 grid((unsigned)(g0 + rows.grid + a.rest_blocks));
   const bool deep = rows.grid + wgrad.grid <= kDeepGrid, wide = f32 || wgrad.split;
-  if (deep && wide)
+  if (rows.bm == 256 && wide)
+    hipLaunchKernelGGL((grouped_grad_kernel<256, 256, 2, 4, 2, EPI_F32, 2, 3>), grid, dim3(512), 0, st, a, b, g0);
+  else if (rows.bm == 256)
+    hipLaunchKernelGGL((grouped_grad_kernel<256, 256, 2, 4, 2, EPI_BF16, 2, 3>), grid, dim3(512), 0, st, a, b, g0);
+  else if (deep && wide)
     hipLaunchKernelGGL((grouped_grad_kernel<128, 128, 2, 2, 1, EPI_F32, 4, 4>), grid, dim3(256), 0, st, a, b, g0);
   else if (deep)
     hipLaunchKernelGGL((grouped_grad_kernel<128, 128, 2, 2, 1, EPI_BF16, 4, 4>), grid, dim3(256), 0, st, a, b, g0);
