@@ -139,6 +139,7 @@ GroupedPlan grouped_rows_plan(int64_t R, int E, int N, int kd, int kstep, bool f
   p.ntiles = (N + bn - 1) / bn;
   p.grid = grouped_max_tiles(R, E, p.bm) * p.ntiles;
   finish_plan(p, E);
+  if (p.bm == 256 && kstep == 64 && p.grid > kCus) p.grid += kTailBlocks;
   const int steps = (kd + kstep - 1) / kstep;
   const int unit = kstep == 64 ? 1 : kstep;             // (codes: pieces in whole blocks)
   if (p.bm <= 128 && p.grid > 0 && p.grid <= kDeepGrid / 2 && steps * kstep >= kSplitMinSteps * 64) {
@@ -339,14 +340,15 @@ hipError_t launch_grouped_wgrad(const GroupedProduct& p, int M, bool f32, bool a
 }
 
 bool grouped_grad_in_one(const GroupedPlan& rows, const GroupedPlan& wgrad) {
-  if (rows.bm == 256 && wgrad.bm == 256) return true;
-  return rows.bm == 128 && wgrad.bm == 128 && rows.scan && wgrad.scan && !rows.ksplit;
+  return rows.bm == wgrad.bm && !rows.ksplit;
 }
 
 hipError_t launch_grouped_grad(const GroupedProduct& dx, const GroupedPlan& rows, bool rest, const GroupedProduct& dw,
                                const GroupedPlan& wgrad, int M, bool f32, bool accumulate, const GroupedScratch& s,
                                hipStream_t st) {
-  const GroupedArgs a = rows_args(dx, rows, s, rest), b = wgrad_args(dw, M, accumulate, wgrad, s);
+  GroupedArgs a = rows_args(dx, rows, s, rest);
+  const GroupedArgs b = wgrad_args(dw, M, accumulate, wgrad, s);
+  a.before = (int)wgrad.grid;
   const int g0 = (int)wgrad.grid;
   const dim3 grid((unsigned)(g0 + rows.grid + a.rest_blocks));
   const bool deep = rows.grid + wgrad.grid <= kDeepGrid, wide = f32 || wgrad.split;

@@ -63,7 +63,7 @@ hipError_t launch_grouped_rows(const GroupedProduct& p, const GroupedPlan& plan,
 hipError_t launch_grouped_wgrad(const GroupedProduct& p, int M, bool f32, bool accumulate, const GroupedPlan& plan,
                                 const GroupedScratch& s, hipStream_t st);
 
-// dx and dW in one launch, where both are small
+// whether one launch can do dx and dW (one tile size)
 bool grouped_grad_in_one(const GroupedPlan& rows, const GroupedPlan& wgrad);
 hipError_t launch_grouped_grad(const GroupedProduct& dx, const GroupedPlan& rows, bool rest, const GroupedProduct& dw,
                                const GroupedPlan& wgrad, int M, bool f32, bool accumulate, const GroupedScratch& s,

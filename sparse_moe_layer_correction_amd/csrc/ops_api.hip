@@ -127,13 +127,18 @@ GroupedLayout forward_layout(const moe_grouped_dims& d, const GroupedPlan& p, bo
 
 struct GradPlans {
   GroupedPlan rows, wgrad;
+  bool one;                  // dx and dw in one launch
   int table_bm;              // of the one table both use (the rows product's tiles; the gradient takes its ranges)
 };
 
 GradPlans grad_plans(const moe_grouped_dims& d, bool dx, bool dw) {
-  GradPlans g{grouped_rows_plan(d.R, d.E, d.K, d.N, 64, false), grouped_wgrad_plan(d.R, d.E, d.N, d.K), 0};
-  // (dx by itself may take the tile for few rows; in one launch with dw both have the same)
-  if (!dx || !dw || !grouped_grad_in_one(g.rows, g.wgrad)) g.rows = grouped_rows_plan(d.R, d.E, d.K, d.N, 64);
+  GradPlans g{grouped_rows_plan(d.R, d.E, d.K, d.N, 64, false), grouped_wgrad_plan(d.R, d.E, d.N, d.K), false, 0};
+  // one launch needs one tile size: few rows take the tile that is theirs, in a
+  // launch of their own, unless both products are small
+  const GroupedPlan alone = grouped_rows_plan(d.R, d.E, d.K, d.N, 64);
+  g.one = dx && dw && grouped_grad_in_one(g.rows, g.wgrad) &&
+          (alone.bm == g.rows.bm || (g.rows.scan && g.wgrad.scan));
+  if (!g.one) g.rows = alone;
   if ((dx && !g.rows.scan) || (dw && !g.wgrad.scan)) g.table_bm = g.rows.bm;
   return g;
 }
@@ -206,7 +211,7 @@ int moe_grouped_matmul_grad(const moe_grouped_dims* dims, const uint16_t* dy, co
   const GroupedProduct px{dy, w, dx, d.ldy, d.ldw, d.lddx, d.w_stride, d.R, d.E, d.K, d.N, true, offsets};
   const GroupedProduct pw{dy, x, dw, d.ldy, d.ldx, d.K, (int64_t)d.N * d.K, d.R, d.E, d.K, 0, true, offsets};
   const bool f32 = dw_dtype == MOE_FP32, rest_rows = d.zero_rest != 0;
-  if (run_dx && dw && grouped_grad_in_one(rows, wg))
+  if (plans.one)
     return hip_status(launch_grouped_grad(px, rows, rest_rows, pw, wg, d.N, f32, accumulate != 0, s, stream));
   if (run_dx && launch_grouped_rows(px, rows, s, rest_rows, stream) != hipSuccess) return MOE_ERR_HIP;
   if (dw && launch_grouped_wgrad(pw, d.N, f32, accumulate != 0, wg, s, stream) != hipSuccess) return MOE_ERR_HIP;
