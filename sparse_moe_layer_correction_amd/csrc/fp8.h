@@ -61,13 +61,11 @@ grouped_fp8_kernel(const Fp8Args P) {
     kb = min(P.klen, P.kb - kt0);
     c_base = piece * P.c_stride;
   }
-  int valid, t;
+  TilePart tp;
   TileRec rec;
   if (P.tiles != nullptr) {
-    valid = *P.n_mtiles * P.ntiles;
-    if (block >= valid) return;
-    t = xcd_remap(block, valid);
-    rec = P.tiles[t / P.ntiles];
+    if (!tp.pick<BM>(block, *P.n_mtiles * P.ntiles, nblocks, 0)) return;
+    rec = P.tiles[tp.t / P.ntiles];
   } else {
     const bool mine = with_scan(P.offsets, P.E, (int)P.R, lane, [&](const auto& scan) {
       const int grid = nblocks - P.rest_blocks;
@@ -77,19 +75,21 @@ grouped_fp8_kernel(const Fp8Args P) {
         return false;
       }
       int incl;
-      valid = scan.tiles(BM, incl) * P.ntiles;
-      if (block >= valid) return false;
-      t = xcd_remap(block, valid);
-      rec = scan.find(BM, t / P.ntiles, incl);
+      if (!tp.pick<BM>(block, scan.tiles(BM, incl) * P.ntiles, grid, 0)) return false;
+      rec = scan.find(BM, tp.t / P.ntiles, incl);
       return true;
     });
     if (!mine) return;
   }
   const int e = __builtin_amdgcn_readfirstlane(rec.x), first = __builtin_amdgcn_readfirstlane(rec.y);
-  const int lo = __builtin_amdgcn_readfirstlane(rec.z), hi = __builtin_amdgcn_readfirstlane(rec.w);
-  int mt, nt;
-  grouped_tile_order(t - first * P.ntiles, (hi - lo + BM - 1) / BM, (hi - lo) / BM, P.ntiles, 8, mt, nt);
-  const int m0 = __builtin_amdgcn_readfirstlane(lo + mt * BM), n0 = __builtin_amdgcn_readfirstlane(nt * BN);
+  const int lo = __builtin_amdgcn_readfirstlane(rec.z);
+  int hi = __builtin_amdgcn_readfirstlane(rec.w), mt, nt;
+  grouped_tile_order(tp.t - first * P.ntiles, (hi - lo + BM - 1) / BM, (hi - lo) / BM, P.ntiles, 8, mt, nt);
+  const int n0 = __builtin_amdgcn_readfirstlane(nt * BN);
+  int m0 = __builtin_amdgcn_readfirstlane(lo + mt * BM);
+  if constexpr (BM == 256) {
+    if (!tp.rows(BM, m0, hi)) return;
+  }
   const int ld2 = P.K / 2, K2 = min(P.K - kt0 * 128, kb * 128) / 2;   // the loads count pairs of codes
 
   // HQ: the tile's height in quarters of BM (1, 2 or 4: an expert's last tile may be short)

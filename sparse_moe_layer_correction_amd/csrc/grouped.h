@@ -347,6 +347,45 @@ __device__ __forceinline__ void store_wave_tile(const f32x16 (&acc)[WTN / 32][WT
   }
 }
 
+// Tile and part of a workgroup, of valid tiles in a grid that has room for more
+// (before: workgroups of the launch that come first). The tiles behind the last
+// full round over the CUs are cut into parts of a half or a quarter of their
+// height, as far as the grid's spare workgroups go: they end sooner on CUs that
+// would idle. us, whole / cut: 544 tiles of 1024 deep sums 84 / 76, 272 of 2048
+// 91 / 74, R 65536 over 64, [2048, 2048] 558 / 545; codes, 272 of 2048 59 / 48. (Not in a first
+// round: half-height tiles on all CUs load half again as much, 126 tiles 31 / 39.)
+struct TilePart {
+  int t, part = 0, parts = 1;
+  template <int BM>
+  __device__ __forceinline__ bool pick(int block, int valid, int grid, int before) {
+    int tail = 0, n = 1;
+    if constexpr (BM == 256) {
+      tail = min((before + valid) % kCus, valid);
+      const int spare = before + valid > kCus ? min(grid - valid, kCus / 2) : 0;   // (half a round at most)
+      n = tail * 3 <= spare ? 4 : tail <= spare ? 2 : 1;
+      if (n == 1) tail = 0;
+    }
+    const int main = valid - tail;
+    if (block >= valid + tail * (n - 1)) return false;
+    if (block < main) {
+      t = xcd_remap(block, main);
+    } else {
+      part = (block - main) / tail;
+      parts = n;
+      t = block - part * tail;
+    }
+    return true;
+  }
+  // the part's rows [m0, mend); false if the tile has none there
+  __device__ __forceinline__ bool rows(int BM, int& m0, int& mend) const {
+    if (parts == 1) return true;
+    const int h = BM / parts;
+    m0 = __builtin_amdgcn_readfirstlane(m0 + part * h);
+    mend = __builtin_amdgcn_readfirstlane(min(mend, m0 + h));
+    return m0 < mend;
+  }
+};
+
 // LDS of a workgroup: AST stages of the rows operand, BST of the other, each an
 // array of its own, so that the compiler can tell the stage being filled from
 // the one being read.
@@ -440,34 +479,9 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& P, int block, in
     Bp = P.B + (int64_t)lo * P.ldb + n0;
     c_base = (int64_t)e * P.c_estride;
   } else {
-    int t, k0 = 0, part = 0, parts = 1;
+    int k0 = 0;
+    TilePart tp;
     TileRec rec;
-    // Tile and part of this workgroup, of valid tiles in a grid that has room for
-    // more. The tiles behind the last full round over the CUs are cut into parts
-    // of a half or a quarter of their height, as far as the grid's spare
-    // workgroups go: they end sooner on CUs that would idle. us, whole / cut: 544
-    // tiles of 1024 deep sums 84 / 76, 272 of 2048 91 / 74, R 65536 over 64,
-    // [2048, 2048] 558 / 545. (Not in a first round: half-height tiles on all
-    // CUs load half again as much, 126 tiles 31 / 39.)
-    auto pick = [&](int valid, int grid) {
-      int tail = 0;
-      if constexpr (BM == 256) {
-        tail = min((P.before + valid) % kCus, valid);
-        const int spare = P.before + valid > kCus ? min(grid - valid, kCus / 2) : 0;   // (half a round at most)
-        parts = tail * 3 <= spare ? 4 : tail <= spare ? 2 : 1;
-        if (parts == 1) tail = 0;
-      }
-      const int main = valid - tail;
-      if (block >= valid + tail * (parts - 1)) return false;
-      if (block < main) {
-        t = xcd_remap(block, main);
-        parts = 1;
-      } else {
-        part = (block - main) / tail;
-        t = block - part * tail;
-      }
-      return true;
-    };
     if (P.ksplit > 1) {
       nblocks /= P.ksplit;
       const int piece = block / nblocks;
@@ -476,8 +490,8 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& P, int block, in
       c_base = piece * P.c_estride;
     }
     if (P.tiles != nullptr) {
-      if (!pick(*P.n_mtiles * P.ntiles, nblocks)) return;
-      rec = P.tiles[t / P.ntiles];
+      if (!tp.pick<BM>(block, *P.n_mtiles * P.ntiles, nblocks, P.before)) return;
+      rec = P.tiles[tp.t / P.ntiles];
     } else {
       const bool mine = with_scan(P.offsets, P.E, P.R, lane, [&](const auto& scan) {
         const int grid = nblocks - P.rest_blocks;
@@ -487,8 +501,8 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& P, int block, in
           return false;
         }
         int incl;
-        if (!pick(scan.tiles(BM, incl) * P.ntiles, grid)) return false;
-        rec = scan.find(BM, t / P.ntiles, incl);
+        if (!tp.pick<BM>(block, scan.tiles(BM, incl) * P.ntiles, grid, P.before)) return false;
+        rec = scan.find(BM, tp.t / P.ntiles, incl);
         return true;
       });
       if (!mine) return;
@@ -496,17 +510,12 @@ __device__ __forceinline__ void grouped_body(const GroupedArgs& P, int block, in
     const int e = __builtin_amdgcn_readfirstlane(rec.x), first = __builtin_amdgcn_readfirstlane(rec.y);
     const int lo = __builtin_amdgcn_readfirstlane(rec.z), hi = __builtin_amdgcn_readfirstlane(rec.w);
     int mt, nt;
-    grouped_tile_order(t - first * P.ntiles, (hi - lo + BM - 1) / BM, (hi - lo) / BM, P.ntiles, 8, mt, nt);
+    grouped_tile_order(tp.t - first * P.ntiles, (hi - lo + BM - 1) / BM, (hi - lo) / BM, P.ntiles, 8, mt, nt);
     m0 = __builtin_amdgcn_readfirstlane(lo + mt * BM);
     n0 = __builtin_amdgcn_readfirstlane(nt * BN);
     mend = hi;
     if constexpr (BM == 256) {
-      if (parts > 1) {
-        const int h = BM / parts;
-        m0 = __builtin_amdgcn_readfirstlane(m0 + part * h);
-        mend = __builtin_amdgcn_readfirstlane(min(hi, m0 + h));
-        if (m0 >= mend) return;
-      }
+      if (!tp.rows(BM, m0, mend)) return;
     }
     Kd = P.ksplit > 1 ? min(P.klen, P.Kd - k0) : P.Kd;
     Ap = P.A + (int64_t)m0 * P.lda + k0;

@@ -139,7 +139,7 @@ GroupedPlan grouped_rows_plan(int64_t R, int E, int N, int kd, int kstep, bool f
   p.ntiles = (N + bn - 1) / bn;
   p.grid = grouped_max_tiles(R, E, p.bm) * p.ntiles;
   finish_plan(p, E);
-  if (p.bm == 256 && kstep == 64 && p.grid > kCus) p.grid += kTailBlocks;
+  if (p.bm == 256 && p.grid > kCus) p.grid += kTailBlocks;
   const int steps = (kd + kstep - 1) / kstep;
   const int unit = kstep == 64 ? 1 : kstep;             // (codes: pieces in whole blocks)
   if (p.bm <= 128 && p.grid > 0 && p.grid <= kDeepGrid / 2 && steps * kstep >= kSplitMinSteps * 64) {
