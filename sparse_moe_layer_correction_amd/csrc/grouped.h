@@ -352,8 +352,9 @@ __device__ __forceinline__ void store_wave_tile(const f32x16 (&acc)[WTN / 32][WT
 // full round over the CUs are cut into parts of a half or a quarter of their
 // height, as far as the grid's spare workgroups go: they end sooner on CUs that
 // would idle. us, whole / cut: 544 tiles of 1024 deep sums 84 / 76, 272 of 2048
-// 91 / 74, R 65536 over 64, [2048, 2048] 558 / 545; codes, 272 of 2048 59 / 48. (Not in a first
-// round: half-height tiles on all CUs load half again as much, 126 tiles 31 / 39.)
+// 91 / 74, R 65536 over 64, [2048, 2048] 558 / 545; codes, 272 of 2048 59 / 48.
+// (Not in a first round: half-height tiles on all CUs load half again as much,
+// 126 tiles 31 / 39.)
 struct TilePart {
   int t, part = 0, parts = 1;
   template <int BM>
