@@ -376,8 +376,8 @@ int moe_grouped_matmul_grad(const moe_grouped_dims* dims, const uint16_t* dy, co
  *   blocks: w [count, N, K] bf16 dense, blocks of 128 x 128:
  *           codes [count, N, K], scales [count, ceil(N/128), ceil(K/128)]
  * MOE_ERR_INVALID: R, count < 0, N, K <= 0, ldx < K, null or not 16-byte aligned
- * x, w, codes, memory shared between them; MOE_ERR_UNSUPPORTED: K or ldx not a multiple of 8, 2^28 blocks of
- * rows or 2^24 blocks of weights or more, N * K >= 2^31. */
+ * x, w, codes, memory shared between them; MOE_ERR_UNSUPPORTED: K or ldx not a multiple of 8, more than 2^28 - 16
+ * blocks of rows, 2^24 blocks of weights or more, N * K >= 2^31. */
 int moe_quantize_fp8_rows(const uint16_t* x, int64_t R, int32_t K, int64_t ldx, uint8_t* codes, float* scales,
                           hipStream_t stream);
 int moe_quantize_fp8_blocks(const uint16_t* w, int64_t count, int32_t N, int32_t K, uint8_t* codes, float* scales,
@@ -412,9 +412,10 @@ typedef struct moe_grad_tensor {
 
 /* norm = sqrt(sum of all tensors' squares), summed in float64 (in an order that
  * the sizes fix) and rounded once to fp32, on the device.
- * moe_clip_grad_norm also writes out = grad * (max_norm / norm), one rounding, if
- * norm > max_norm and norm is finite, and out = grad otherwise. The host array
- * `tensors` is read during the call only. Nothing waits for the GPU.
+ * moe_clip_grad_norm also writes out = grad * (max_norm / norm), computed in
+ * float64 and rounded to the type (bf16 by way of fp32), if norm > max_norm and
+ * norm is finite, and out = grad otherwise. The host array `tensors` is read
+ * during the call only. Nothing waits for the GPU.
  * MOE_ERR_INVALID: count < 0, null tensors with count > 0, a null, misaligned or
  * negative-length tensor, an unknown dtype, max_norm negative or NaN, a null
  * norm, or (clip) outputs, the norm among them, that overlap each other or another gradient.

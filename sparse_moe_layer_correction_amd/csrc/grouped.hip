@@ -340,7 +340,7 @@ hipError_t launch_grouped_wgrad(const GroupedProduct& p, int M, bool f32, bool a
 }
 
 bool grouped_grad_in_one(const GroupedPlan& rows, const GroupedPlan& wgrad) {
-  return rows.bm == wgrad.bm && !rows.ksplit;
+  return rows.bm == wgrad.bm && !rows.ksplit && rows.grid + wgrad.grid < kMaxGrid;
 }
 
 hipError_t launch_grouped_grad(const GroupedProduct& dx, const GroupedPlan& rows, bool rest, const GroupedProduct& dw,

@@ -10,8 +10,8 @@ struct GroupedScratch {
   int2* ranges;        // [E] rows of each expert
   int4* tiles;         // [grouped_max_tiles] M tile table
   int32_t* n_mtiles;   // [1]
-  float* partial;      // sums of the pieces of a split weight gradient, or (after them) of a split rows product
-  float* row_partial;
+  float* partial;      // sums of the pieces of a split weight gradient
+  float* row_partial;  // sums of the pieces of a split rows product
 };
 
 // M tiles that R rows in E experts can need
@@ -27,6 +27,9 @@ struct GroupedProduct {
   bool transposed_b;   // B stored [Kd, N]
   const int32_t* offsets;
 };
+
+// a grid's threads are counted in 32 bits; workgroups have up to 512
+constexpr int64_t kMaxGrid = (int64_t)1 << 23;
 
 // Tiles and grid of one product.
 struct GroupedPlan {

@@ -24,9 +24,7 @@ bool ws_ok(const void* ws, size_t have, size_t need) {
 }
 bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
 
-// a grid's threads are counted in 32 bits; workgroups have up to 512
-constexpr int64_t kMaxGrid = (int64_t)1 << 23;
-constexpr int64_t kMaxBlocks = (int64_t)1 << 28;   // 16 to a workgroup of 256 threads
+constexpr int64_t kMaxBlocks = ((int64_t)1 << 28) - 16;   // 16 to a workgroup of 256 threads, whose number is 32 bits
 constexpr int64_t kMaxStride = (int64_t)1 << 21;   // 256 rows of 2 bytes and their k offsets stay below 2 GiB
 constexpr int64_t kMaxRows = (int64_t)1 << 30;     // row counts round up to whole tiles in 32 bits
 
@@ -223,7 +221,7 @@ int moe_quantize_fp8_rows(const uint16_t* x, int64_t R, int32_t K, int64_t ldx, 
   if (R < 0 || K <= 0 || ldx < 0) return MOE_ERR_INVALID;
   if (ldx == 0) ldx = K;
   if (ldx < K || (R > 0 && (!x || !codes || !scales)) || !aligned16(x) || !aligned16(codes)) return MOE_ERR_INVALID;
-  if (K % 8 || ldx % 8 || R >= kMaxBlocks / ((K + 127) / 128)) return MOE_ERR_UNSUPPORTED;
+  if (K % 8 || ldx % 8 || R > kMaxBlocks / ((K + 127) / 128)) return MOE_ERR_UNSUPPORTED;
   const Region rq = dense_region(codes, R * K), rs = dense_region(scales, R * ((K + 127) / 128) * 4);
   const Region rx = rows_region(x, R, K, ldx, 2);
   if (R > 0 && (overlap(rx, rq) || overlap(rx, rs) || overlap(rq, rs))) return MOE_ERR_INVALID;
@@ -258,7 +256,7 @@ int fp8_impl(const moe_grouped_dims* dims, bool quantise, const uint16_t* x, con
   const int st = grouped_dims(&d, &d);
   if (st != MOE_OK) return st;
   if (d.K % 16) return MOE_ERR_UNSUPPORTED;
-  if (quantise && d.R >= kMaxBlocks / ((d.K + 127) / 128)) return MOE_ERR_UNSUPPORTED;
+  if (quantise && d.R > kMaxBlocks / ((d.K + 127) / 128)) return MOE_ERR_UNSUPPORTED;
   if (!wq || !w_scale || !offsets || (d.R > 0 && (!y || (quantise ? !x : !xq || !xs)))) return MOE_ERR_INVALID;
   if (!aligned16(x) || !aligned16(xq) || !aligned16(wq) || !aligned16(y)) return MOE_ERR_INVALID;
   const GroupedPlan plan = grouped_rows_plan(d.R, d.E, d.N, d.K, 128);

@@ -650,6 +650,11 @@ PLANS = [
     (60000, 150, 1032, 64, ragged(60000, 150, 8, 20)),
     (30000, 2, 136, 64, [29999, 1]),
     (1000, 100, 520, 1040, ragged(1000, 100, 9, 40)),
+    (8100, 4, 1832, 144, [4000, 100, 3000, 1000]),             # 264 tiles of 256 x 256: the last 8 in quarters
+    (8700, 4, 1832, 144, [4000, 200, 3300, 1200]),             # 280: the last 24 in halves
+    (8100, 4, 144, 1840, [4000, 100, 3000, 1000]),
+    (8700, 8, 1800, 1840, [4000, 200, 0, 3200, 100, 0, 1200, 0]),   # both gradients in one launch, with parts
+    (33000, 140, 512, 528, ragged(33000, 140, 10, 20)),        # the same with a tile table
     (300, 100, 72, 2064, [33, 0, 64, 32, 31, 1] + [2] * 69 + [1] + [0] * 24),
 ]
 

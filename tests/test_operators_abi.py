@@ -101,7 +101,9 @@ def test_quantisers(lib):
     assert r(256, 4, 64, 0, 264, 256, None) == -1
     assert r(256, 4, 60, 0, 256, 256, None) == -2
     assert r(256, 4, 64, 68, 256, 256, None) == -2
-    assert r(256, 1 << 28, 64, 0, 256, 256, None) == -2
+    for R, K in (((1 << 28) - 15, 64), ((1 << 27) - 7, 136)):    # one more than the grid's threads can be counted for
+        assert r(1 << 40, R, K, 0, 1 << 44, 1 << 46, None) == -2
+        assert r(1 << 40, R - 1, K, 0, 1 << 40, 1 << 46, None) == -1       # (refused for the shared memory alone)
     assert b(256, -1, 64, 64, 256, 256, None) == -1
     assert b(256, 1, 64, 0, 256, 256, None) == -1
     assert b(256, 1, 64, 64, None, 256, None) == -1
