@@ -392,8 +392,8 @@ int moe_grouped_matmul_fp8(const moe_grouped_dims* dims, const uint8_t* xq, cons
                            const float* w_scale, const int32_t* offsets, uint16_t* y, void* ws, size_t ws_bytes,
                            hipStream_t stream);
 
-/* The same from bf16 rows x [R, K] (row stride ldx): moe_quantize_fp8_rows into
- * the workspace, then the product; the same bits. */
+/* The same from bf16 rows x [R, K] (row stride ldx), whose codes and scales, those
+ * of moe_quantize_fp8_rows, are made in the workspace; the same bits. */
 int moe_grouped_matmul_fp8_rows(const moe_grouped_dims* dims, const uint16_t* x, const uint8_t* wq,
                                 const float* w_scale, const int32_t* offsets, uint16_t* y, void* ws, size_t ws_bytes,
                                 hipStream_t stream);

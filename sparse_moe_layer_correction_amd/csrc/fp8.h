@@ -8,6 +8,70 @@ namespace moe {
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
+// exponent e of the block scale 2^e: the least with amax <= 448 * 2^e, not below
+// -126 (the scale stays a normal number). 448 = 0.875 * 2^9. A power of two loses
+// nothing against amax / 448 (E4M3's precision is relative; a block gives up at
+// most one bit of its range), and scaling by it is exact, so the codes are the
+// definition's own, with one rounding each.
+__device__ __forceinline__ int fp8_block_exponent(float amax) {
+  if (!(amax > 0.f)) return -126;
+  const int ex = __builtin_amdgcn_frexp_expf(amax);
+  const float mant = __builtin_amdgcn_frexp_mantf(amax);
+  return max(mant > 0.875f ? ex - 8 : ex - 9, -126);
+}
+
+// Four values of magnitude at most 448 as E4M3 codes (round to nearest even);
+// a value that is not finite becomes the NaN code.
+__device__ __forceinline__ uint32_t fp8_pack4(const float (&v)[4]) {
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], w, true);
+  uint32_t u = (uint32_t)w;
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    if (!(fabsf(v[i]) <= 448.f)) u |= 0x7Fu << (8 * i);
+  return u;
+}
+
+__device__ __forceinline__ float finite_abs(uint32_t bf16_bits) {
+  const uint32_t a = bf16_bits & 0x7FFFu;
+  return a < 0x7F80u ? __uint_as_float(a << 16) : 0.f;
+}
+
+// max |v| over the finite values of 8 bf16
+__device__ __forceinline__ float amax8(const u32x4 w) {
+  float a = 0.f;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) a = fmaxf(a, fmaxf(finite_abs(w[q] & 0xFFFFu), finite_abs(w[q] >> 16)));
+  return a;
+}
+
+__device__ __forceinline__ u32x2 codes8(const u32x4 w, float inv) {
+  u32x2 o;
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    const float v[4] = {bf16_bits_to_f32(w[2 * h] & 0xFFFFu) * inv, bf16_bits_to_f32(w[2 * h] >> 16) * inv,
+                        bf16_bits_to_f32(w[2 * h + 1] & 0xFFFFu) * inv, bf16_bits_to_f32(w[2 * h + 1] >> 16) * inv};
+    o[h] = fp8_pack4(v);
+  }
+  return o;
+}
+
+// Block b of a row, 16 lanes with 8 values each.
+__device__ __forceinline__ u32x4 load_block(const uint16_t* row, int b, int K) {
+  const int k = b * 128 + (threadIdx.x & 15) * 8;
+  return k < K ? *reinterpret_cast<const u32x4*>(row + k) : u32x4{0u, 0u, 0u, 0u};
+}
+// Its codes and its scale. The 16 lanes are together.
+__device__ __forceinline__ void quantise_block(const u32x4 w, uint8_t* row, int b, int K, float* scale) {
+  const int k = b * 128 + (threadIdx.x & 15) * 8;
+  float a = amax8(w);
+#pragma unroll
+  for (int m = 8; m >= 1; m >>= 1) a = fmaxf(a, __shfl_xor(a, m, kWave));
+  const int e = fp8_block_exponent(a);
+  if (k < K) *reinterpret_cast<u32x2*>(row + k) = codes8(w, __builtin_ldexpf(1.f, -e));
+  if ((threadIdx.x & 15) == 0) *scale = __builtin_ldexpf(1.f, e);
+}
+
 // s_waitcnt vmcnt(n) lgkmcnt(0), and lgkmcnt(0) alone
 constexpr int wait_lgkm0(int n) { return (n & 0xF) | (0x7 << 4) | (((n >> 4) & 3) << 14); }
 constexpr int kWaitLgkm0 = 0xF | (0x7 << 4) | (3 << 14);
@@ -89,6 +153,32 @@ grouped_fp8_kernel(const Fp8Args P) {
   int m0 = __builtin_amdgcn_readfirstlane(lo + mt * BM);
   if constexpr (BM == 256) {
     if (!tp.rows(BM, m0, hi)) return;
+  }
+  if constexpr (BM == 32) {
+    if (P.x != nullptr) {
+      // Few rows, quantised here: every workgroup makes the codes and scales that
+      // it reads itself (those of other column tiles store the same bytes), and
+      // no launch comes before this one. Four blocks a 16 lanes at a time, their
+      // loads together.
+      constexpr int NG = NT / 16;
+      const int n = min(hi - m0, BM) * kb;
+      for (int i = tid / 16; i < n; i += 4 * NG) {
+        u32x4 w[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int j = min(i + q * NG, n - 1), r = j / kb;
+          w[q] = load_block(P.x + (int64_t)(m0 + r) * P.ldx, kt0 + j - r * kb, P.K);
+        }
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int j = min(i + q * NG, n - 1), r = j / kb, b = kt0 + j - r * kb;
+          quantise_block(w[q], const_cast<uint8_t*>(P.A) + (int64_t)(m0 + r) * P.K, b, P.K,
+                         const_cast<float*>(P.sx) + (int64_t)b * P.R + m0 + r);
+        }
+      }
+      __threadfence_block();
+      __syncthreads();
+    }
   }
   const int ld2 = P.K / 2, K2 = min(P.K - kt0 * 128, kb * 128) / 2;   // the loads count pairs of codes
 

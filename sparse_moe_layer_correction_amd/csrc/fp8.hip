@@ -18,54 +18,6 @@
 
 namespace moe {
 
-// exponent e of the block scale 2^e: the least with amax <= 448 * 2^e, not below
-// -126 (the scale stays a normal number). 448 = 0.875 * 2^9. A power of two loses
-// nothing against amax / 448 (E4M3's precision is relative; a block gives up at
-// most one bit of its range), and scaling by it is exact, so the codes are the
-// definition's own, with one rounding each.
-__device__ __forceinline__ int fp8_block_exponent(float amax) {
-  if (!(amax > 0.f)) return -126;
-  const int ex = __builtin_amdgcn_frexp_expf(amax);
-  const float mant = __builtin_amdgcn_frexp_mantf(amax);
-  return max(mant > 0.875f ? ex - 8 : ex - 9, -126);
-}
-
-// Four values of magnitude at most 448 as E4M3 codes (round to nearest even);
-// a value that is not finite becomes the NaN code.
-__device__ __forceinline__ uint32_t fp8_pack4(const float (&v)[4]) {
-  int w = __builtin_amdgcn_cvt_pk_fp8_f32(v[0], v[1], 0, false);
-  w = __builtin_amdgcn_cvt_pk_fp8_f32(v[2], v[3], w, true);
-  uint32_t u = (uint32_t)w;
-#pragma unroll
-  for (int i = 0; i < 4; ++i)
-    if (!(fabsf(v[i]) <= 448.f)) u |= 0x7Fu << (8 * i);
-  return u;
-}
-
-__device__ __forceinline__ float finite_abs(uint32_t bf16_bits) {
-  const uint32_t a = bf16_bits & 0x7FFFu;
-  return a < 0x7F80u ? __uint_as_float(a << 16) : 0.f;
-}
-
-// max |v| over the finite values of 8 bf16
-__device__ __forceinline__ float amax8(const u32x4 w) {
-  float a = 0.f;
-#pragma unroll
-  for (int q = 0; q < 4; ++q) a = fmaxf(a, fmaxf(finite_abs(w[q] & 0xFFFFu), finite_abs(w[q] >> 16)));
-  return a;
-}
-
-__device__ __forceinline__ u32x2 codes8(const u32x4 w, float inv) {
-  u32x2 o;
-#pragma unroll
-  for (int h = 0; h < 2; ++h) {
-    const float v[4] = {bf16_bits_to_f32(w[2 * h] & 0xFFFFu) * inv, bf16_bits_to_f32(w[2 * h] >> 16) * inv,
-                        bf16_bits_to_f32(w[2 * h + 1] & 0xFFFFu) * inv, bf16_bits_to_f32(w[2 * h + 1] >> 16) * inv};
-    o[h] = fp8_pack4(v);
-  }
-  return o;
-}
-
 // Rows x [R, K] (row stride ldx) to codes [R, K] and scales [ceil(K / 128), R].
 // 16 lanes take a block of 128 (16 bytes each), so a wave reads 1 KB of a row;
 // the scales of 16 consecutive rows are written together.
@@ -76,15 +28,7 @@ __global__ void __launch_bounds__(256) fp8_rows_kernel(const uint16_t* __restric
   const int64_t r = blk / kb;
   const int b = (int)(blk - r * kb);
   if (r >= R) return;                                  // whole 16-lane groups leave together
-  const int k = b * 128 + (threadIdx.x & 15) * 8;
-  u32x4 w{0u, 0u, 0u, 0u};
-  if (k < K) w = *reinterpret_cast<const u32x4*>(x + r * ldx + k);
-  float a = amax8(w);
-#pragma unroll
-  for (int m = 8; m >= 1; m >>= 1) a = fmaxf(a, __shfl_xor(a, m, kWave));
-  const int e = fp8_block_exponent(a);
-  if (k < K) *reinterpret_cast<u32x2*>(codes + r * K + k) = codes8(w, __builtin_ldexpf(1.f, -e));
-  if ((threadIdx.x & 15) == 0) scales[(int64_t)b * R + r] = __builtin_ldexpf(1.f, e);
+  quantise_block(load_block(x + r * ldx, b, K), codes + r * K, b, K, scales + (int64_t)b * R + r);
 }
 
 hipError_t launch_fp8_rows(const uint16_t* x, int64_t R, int K, int64_t ldx, uint8_t* codes, float* scales,
@@ -138,6 +82,18 @@ hipError_t launch_fp8_blocks(const uint16_t* w, int64_t count, int N, int K, uin
   if (grid == 0) return hipSuccess;
   hipLaunchKernelGGL(fp8_blocks_kernel, dim3((unsigned)grid), dim3(256), 0, st, w, N, K, nb, kb, codes, scales);
   return hipGetLastError();
+}
+
+// Every column tile of a row quantises it again, so few blocks for each
+// workgroup (with a tile full of rows) and for all of them. us of a call, the
+// quantiser's launch / its own: R 64, E 16, [512, 512] (128 blocks, 9 K) 10.6 / 7.9,
+// R 300, E 20, [1000, 256] (64, 15 K) 10.7 / 8.1, E 8, [5000, 128] (32, 22 K) 10.9 /
+// 9.7; R 400, E 64, [1024, 512] (128, 78 K) 10.5 / 11.9, R 22, E 512, [5120, 2048]
+// (352, 310 K) 42.8 / 45.0, R 30, E 4, [2048, 5120] (300, split) 15.0 / 16.6.
+constexpr int64_t kOwnBlocks = 128, kOwnTotal = 32768;
+bool fp8_quantises(const GroupedPlan& plan, int64_t R, int K) {
+  const int64_t blocks = std::min<int64_t>(R, 32) * (plan.ksplit ? plan.klen : (K + 127) / 128);
+  return plan.bm == 32 && blocks <= kOwnBlocks && plan.grid * std::max(1, plan.ksplit) * blocks <= kOwnTotal;
 }
 
 hipError_t launch_grouped_fp8(const Fp8Args& a, const GroupedPlan& plan, hipStream_t st) {

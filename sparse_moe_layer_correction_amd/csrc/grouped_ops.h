@@ -76,6 +76,8 @@ hipError_t launch_grouped_grad(const GroupedProduct& dx, const GroupedPlan& rows
 struct Fp8Args {
   const uint8_t* A;            // [R, K] codes of the rows
   const float* sx;             // [kb, R]
+  const uint16_t* x;           // 32-row tiles: not null, the bf16 rows (row stride ldx) that A and sx are made of first
+  int64_t ldx;
   const uint8_t* B;            // [E, N, K] codes of the weights
   const float* sw;             // [E, nb, kb]
   void* C;                     // bf16, or (a split reduction) the pieces' fp32 sums
@@ -93,6 +95,8 @@ hipError_t launch_fp8_rows(const uint16_t* x, int64_t R, int K, int64_t ldx, uin
                            hipStream_t st);
 hipError_t launch_fp8_blocks(const uint16_t* w, int64_t count, int N, int K, uint8_t* codes, float* scales,
                              hipStream_t st);
+// whether the product quantises its rows itself
+bool fp8_quantises(const GroupedPlan& plan, int64_t R, int K);
 hipError_t launch_grouped_fp8(const Fp8Args& a, const GroupedPlan& plan, hipStream_t st);
 
 // Gradient tensors of one launch; entry i's chunks of 2^chunk_log2 elements are

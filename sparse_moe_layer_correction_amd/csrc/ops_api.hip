@@ -270,10 +270,11 @@ int fp8_impl(const moe_grouped_dims* dims, bool quantise, const uint16_t* x, con
     return MOE_ERR_INVALID;
   if (d.R == 0) return MOE_OK;
   const GroupedScratch s = grouped_scratch(l, ws);
+  const bool own = quantise && fp8_quantises(plan, d.R, d.K);
   if (quantise) {
     uint8_t* codes = static_cast<uint8_t*>(ws) + l.codes;
     float* scales = reinterpret_cast<float*>(static_cast<char*>(ws) + l.scales);
-    if (launch_fp8_rows(x, d.R, d.K, d.ldx, codes, scales, stream) != hipSuccess) return MOE_ERR_HIP;
+    if (!own && launch_fp8_rows(x, d.R, d.K, d.ldx, codes, scales, stream) != hipSuccess) return MOE_ERR_HIP;
     xq = codes;
     xs = scales;
   }
@@ -283,6 +284,8 @@ int fp8_impl(const moe_grouped_dims* dims, bool quantise, const uint16_t* x, con
   Fp8Args a{};
   a.A = xq;
   a.sx = xs;
+  a.x = own ? x : nullptr;
+  a.ldx = d.ldx;
   a.B = wq;
   a.sw = w_scale;
   a.C = y;

@@ -421,6 +421,33 @@ def test_grouped_matmul_fp8(R, E, N, K, counts):
     assert torch.equal(y, M.grouped_matmul_fp8(codes, wq, sw, o, x_scale=scales))
 
 
+@pytest.mark.parametrize("R,E,N,K,counts", [
+    (16, 8, 2680, 96, [0, 0, 9, 0, 1, 0, 6, 0]),
+    (1, 3, 136, 2064, [0, 1, 0]),
+    (22, 300, 520, 1040, [1 if e % 14 == 3 else 0 for e in range(300)]),
+    (200, 16, 520, 512, [70, 0, 33, 32, 31, 1, 0, 0, 20, 5, 5, 1, 1, 1, 0, 0]),
+    (32, 1, 1000, 2048, [32]), (31, 4, 264, 5072, [3, 0, 27, 1]), (300, 20, 1000, 128, [15] * 20),
+    (150, 5, 2000, 256, [33, 0, 64, 3, 50]), (7, 2, 136, 2064, [4, 3]),
+])
+def test_fp8_few_rows(R, E, N, K, counts):
+    """Few rows are quantised by the product itself: the same bits as from codes made before, call after call in one
+    workspace, with every column tile's workgroups at it at once."""
+    o = offs(counts)
+    wq, sw = M.quantize_fp8_blocks(rnd((E, N, K), 2, K ** -0.5))
+    ws = torch.full((M.grouped_workspace_bytes(R, E, N, K),), 255, dtype=torch.uint8, device="cuda")
+    for rep in range(4):
+        x = rnd((R, K + 8), 10 + rep, 10.0 ** (rep - 2))[:, :K]
+        if rep == 3:
+            x[:, :16] = 0
+            x[R // 2, K - 3] = float("inf")
+        codes, scales = M.quantize_fp8_rows(x)
+        want = M.grouped_matmul_fp8(codes, wq, sw, o, x_scale=scales)
+        assert torch.isfinite(want).all() or rep == 3
+        bits = lambda t: t.view(torch.int16)
+        assert torch.equal(bits(M.grouped_matmul_fp8(x, wq, sw, o, ws=ws)), bits(want))
+        assert torch.equal(bits(M.grouped_matmul_fp8(x, wq, sw, o)), bits(want))
+
+
 @pytest.mark.parametrize("K", [272, 2064])
 def test_fp8_rows_of_no_expert_and_special_values(K):
     R, E, N = 300, 3, 136
