@@ -742,14 +742,15 @@ grouped_kernel(const GroupedArgs P) {
 // The two are independent, and what one leaves idle the other fills: the CUs
 // beside a long expert's dW, whose tiles start first, and those of dx's last
 // tiles.
-template <int BM, int BN, int WM, int WN, int OCC, int OUT, int AST, int BST>
+// (DXO: of dx; EPI_F32 for the pieces of a split reduction)
+template <int BM, int BN, int WM, int WN, int OCC, int DXO, int OUT, int AST, int BST>
 __global__ void __launch_bounds__(64 * WM * WN, 1) __attribute__((amdgpu_waves_per_eu(OCC, OCC)))
 grouped_grad_kernel(const GroupedArgs DX, const GroupedArgs DW, int g0) {
   MOE_GROUPED_LDS(BM, BN, AST, BST);
   if ((int)blockIdx.x < g0)
     grouped_body<FORM_TN, BM, BN, WM, WN, OUT, AST, BST>(DW, blockIdx.x, g0, lds);
   else
-    grouped_body<FORM_NN, BM, BN, WM, WN, EPI_BF16, AST, BST>(DX, (int)blockIdx.x - g0, (int)gridDim.x - g0, lds);
+    grouped_body<FORM_NN, BM, BN, WM, WN, DXO, AST, BST>(DX, (int)blockIdx.x - g0, (int)gridDim.x - g0, lds);
 }
 
 }  // namespace moe

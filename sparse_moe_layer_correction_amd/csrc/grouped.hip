@@ -340,7 +340,29 @@ hipError_t launch_grouped_wgrad(const GroupedProduct& p, int M, bool f32, bool a
 }
 
 bool grouped_grad_in_one(const GroupedPlan& rows, const GroupedPlan& wgrad) {
-  return rows.bm == wgrad.bm && !rows.ksplit && rows.grid + wgrad.grid < kMaxGrid;
+  return rows.bm == wgrad.bm && rows.grid + wgrad.grid < kMaxGrid;
+}
+
+template <int BM, int BN, int WM, int WN, int OCC, int AST, int BST>
+static void launch_grad_form(const GroupedArgs& a, const GroupedArgs& b, int g0, dim3 grid, bool wide, hipStream_t st) {
+  constexpr int NT = 64 * WM * WN;
+  if constexpr (BM == 128) {
+    if (a.ksplit) {
+      if (wide)
+        hipLaunchKernelGGL((grouped_grad_kernel<BM, BN, WM, WN, OCC, EPI_F32, EPI_F32, AST, BST>), grid, dim3(NT), 0,
+                           st, a, b, g0);
+      else
+        hipLaunchKernelGGL((grouped_grad_kernel<BM, BN, WM, WN, OCC, EPI_F32, EPI_BF16, AST, BST>), grid, dim3(NT), 0,
+                           st, a, b, g0);
+      return;
+    }
+  }
+  if (wide)
+    hipLaunchKernelGGL((grouped_grad_kernel<BM, BN, WM, WN, OCC, EPI_BF16, EPI_F32, AST, BST>), grid, dim3(NT), 0, st,
+                       a, b, g0);
+  else
+    hipLaunchKernelGGL((grouped_grad_kernel<BM, BN, WM, WN, OCC, EPI_BF16, EPI_BF16, AST, BST>), grid, dim3(NT), 0, st,
+                       a, b, g0);
 }
 
 hipError_t launch_grouped_grad(const GroupedProduct& dx, const GroupedPlan& rows, bool rest, const GroupedProduct& dw,
@@ -350,21 +372,16 @@ hipError_t launch_grouped_grad(const GroupedProduct& dx, const GroupedPlan& rows
   const GroupedArgs b = wgrad_args(dw, M, accumulate, wgrad, s);
   a.before = (int)wgrad.grid;
   const int g0 = (int)wgrad.grid;
-  const dim3 grid((unsigned)(g0 + rows.grid + a.rest_blocks));
-  const bool deep = rows.grid + wgrad.grid <= kDeepGrid, wide = f32 || wgrad.split;
-  if (rows.bm == 256 && wide)
-    hipLaunchKernelGGL((grouped_grad_kernel<256, 256, 2, 4, 2, EPI_F32, 2, 3>), grid, dim3(512), 0, st, a, b, g0);
-  else if (rows.bm == 256)
-    hipLaunchKernelGGL((grouped_grad_kernel<256, 256, 2, 4, 2, EPI_BF16, 2, 3>), grid, dim3(512), 0, st, a, b, g0);
-  else if (deep && wide)
-    hipLaunchKernelGGL((grouped_grad_kernel<128, 128, 2, 2, 1, EPI_F32, 4, 4>), grid, dim3(256), 0, st, a, b, g0);
-  else if (deep)
-    hipLaunchKernelGGL((grouped_grad_kernel<128, 128, 2, 2, 1, EPI_BF16, 4, 4>), grid, dim3(256), 0, st, a, b, g0);
-  else if (wide)
-    hipLaunchKernelGGL((grouped_grad_kernel<128, 128, 2, 2, 2, EPI_F32, 2, 2>), grid, dim3(256), 0, st, a, b, g0);
-  else
-    hipLaunchKernelGGL((grouped_grad_kernel<128, 128, 2, 2, 2, EPI_BF16, 2, 2>), grid, dim3(256), 0, st, a, b, g0);
-  const hipError_t e = hipGetLastError();
+  const int64_t gx = rows.grid * std::max(1, rows.ksplit) + a.rest_blocks;
+  const dim3 grid((unsigned)(g0 + gx));
+  const bool deep = g0 + gx <= kDeepGrid;
+  if (rows.bm == 256) launch_grad_form<256, 256, 2, 4, 2, 2, 3>(a, b, g0, grid, f32 || wgrad.split, st);
+  else if (deep) launch_grad_form<128, 128, 2, 2, 1, 4, 4>(a, b, g0, grid, f32 || wgrad.split, st);
+  else launch_grad_form<128, 128, 2, 2, 2, 2, 2>(a, b, g0, grid, f32 || wgrad.split, st);
+  hipError_t e = hipGetLastError();
+  if (e == hipSuccess && rows.ksplit)
+    e = launch_rows_join(s.row_partial, rows, dx.R, dx.N, dx.offsets, dx.E, static_cast<uint16_t*>(dx.C), dx.ldc, rest,
+                         st);
   if (e != hipSuccess || !wgrad.split) return e;
   return launch_join(dw, M, f32, accumulate, wgrad, s, st);
 }
