@@ -195,10 +195,10 @@ hipError_t launch_rows_join(const float* partial, const GroupedPlan& plan, int64
 // rows) sums pieces of each expert's rows side by side, as many as give every
 // CU a workgroup, and joins them in row order: [640, 640] x 2 experts over
 // 20000 rows 62 us in one piece each. Pieces are multiples of a k tile, 256 rows or more.
-GroupedPlan grouped_wgrad_plan(int64_t R, int E, int M, int N) {
+GroupedPlan grouped_wgrad_plan(int64_t R, int E, int M, int N, bool big) {
   GroupedPlan p{};
   const bool fits = up(M, 256) * up(N, 256) <= kBigPadding * up(M, 128) * up(N, 128);
-  p.bm = (int64_t)E * ((M + 255) / 256) * ((N + 255) / 256) >= kBigTiles && fits ? 256 : 128;
+  p.bm = big && (int64_t)E * ((M + 255) / 256) * ((N + 255) / 256) >= kBigTiles && fits ? 256 : 128;
   p.mtiles = (M + p.bm - 1) / p.bm;
   p.ntiles = (N + p.bm - 1) / p.bm;
   const int64_t tiles = (int64_t)p.mtiles * p.ntiles;

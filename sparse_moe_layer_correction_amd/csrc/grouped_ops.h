@@ -44,7 +44,8 @@ struct GroupedPlan {
 constexpr int kScanRestBlocks = 16;   // workgroups that zero the rows of no expert, without a table
 // kd: the reduction's length; kstep: of a k tile (64, or 128 codes); few: the tile for few rows may be taken
 GroupedPlan grouped_rows_plan(int64_t R, int E, int N, int kd, int kstep, bool few = true);
-GroupedPlan grouped_wgrad_plan(int64_t R, int E, int M, int N);
+// big: 256 x 256 tiles may be taken
+GroupedPlan grouped_wgrad_plan(int64_t R, int E, int M, int N, bool big = true);
 size_t grouped_partial_bytes(const GroupedPlan& p, int M, int N);
 size_t grouped_row_partial_bytes(const GroupedPlan& p, int64_t R, int N);
 // C = the sum of a split rows product's pieces, over the rows of experts; rest: zero the others

@@ -123,6 +123,12 @@ GroupedLayout forward_layout(const moe_grouped_dims& d, const GroupedPlan& p, bo
   return grouped_layout(d, d.R > 0 ? table_of(p) : 0, 0, grouped_row_partial_bytes(p, d.R, d.N), quantise);
 }
 
+// Rows per expert up to which dW gives up its big tiles to share a launch with a
+// dx of small ones. us, two launches / one: R 2000, E 20, [1000, 704] 34.4 / 28.3,
+// 230 x 4, [1824, 2096] 36 / 30, 363 x 3, [1112, 2344] 28.4 / 25.1; 3000 x 3,
+// [2048, 2048] 64 / 67.
+constexpr int64_t kJointRows = 256;
+
 struct GradPlans {
   GroupedPlan rows, wgrad;
   bool one;                  // dx and dw in one launch
@@ -134,6 +140,10 @@ GradPlans grad_plans(const moe_grouped_dims& d, bool dx, bool dw) {
   // one launch needs one tile size: few rows take the tile that is theirs, in a
   // launch of their own, unless both products are small
   const GroupedPlan alone = grouped_rows_plan(d.R, d.E, d.K, d.N, 64);
+  if (dx && dw && g.rows.bm == 128 && g.wgrad.bm == 256 && d.R <= d.E * kJointRows) {
+    const GroupedPlan small = grouped_wgrad_plan(d.R, d.E, d.N, d.K, false);
+    if (g.rows.scan && small.scan) g.wgrad = small;
+  }
   g.one = dx && dw && grouped_grad_in_one(g.rows, g.wgrad) &&
           (alone.bm == g.rows.bm || (g.rows.scan && g.wgrad.scan));
   if (!g.one) g.rows = alone;

@@ -682,6 +682,9 @@ PLANS = [
     (8100, 4, 144, 1840, [4000, 100, 3000, 1000]),
     (8700, 8, 1800, 1840, [4000, 200, 0, 3200, 100, 0, 1200, 0]),   # both gradients in one launch, with parts
     (33000, 140, 512, 528, ragged(33000, 140, 10, 20)),        # the same with a tile table
+    (1000, 8, 2048, 256, ragged(1000, 8, 11, 1)),              # one launch: a split dx beside dW
+    (2008, 3, 3032, 304, [1500, 0, 508]),                      # and both split
+    (230, 4, 1824, 2096, [60, 100, 0, 70]),                    # dW in small tiles for it
     (300, 100, 72, 2064, [33, 0, 64, 32, 31, 1] + [2] * 69 + [1] + [0] * 24),
 ]
 
@@ -717,4 +720,7 @@ def test_every_plan(R, E, N, K, counts):
     M.grouped_matmul_grad(dy, x, w, o, need_dx=False, dw=dw, accumulate=True)
     M.grouped_matmul_grad(dy, x, w, o, need_dx=False, dw=dwb, accumulate=True)
     assert torch.equal(dw, 2 * keep)
+    joint = keep.clone()                                       # and beside dx
+    dx2, _ = M.grouped_matmul_grad(dy, x, w, o, dw=joint, accumulate=True)
+    assert torch.equal(dx2, dx) and torch.equal(joint, 2 * keep)
     assert ((dwb.double() - 2 * keepb.double()).abs() <= 2.0 ** -7 * 2 * keepb.double().abs()).all()
