@@ -10,6 +10,8 @@
 // workgroup, then the workgroups' partials in order), so a call repeats bit
 // for bit.
 //
+// Small lists are one launch of one workgroup, whose waves take the chunks.
+//
 // The tensors' addresses travel in the kernel arguments (kGradTableSize a
 // launch): nothing is copied to the device, and nothing of them is kept.
 #include "grouped_ops.h"
@@ -54,12 +56,11 @@ __device__ __forceinline__ int head_of(const T* p, int n) {
   return min(mis, n);
 }
 
-template <int SIZE>
-__global__ void __launch_bounds__(kGradThreads) grad_sumsq_kernel(const GradTableOf<SIZE> t,
-                                                                  double* __restrict__ partial) {
-  __shared__ double part[kGradThreads / kWave];
+// a thread's part of the sum of squares, thread tid of the NT of group `block` of `blocks`
+template <int NT, int SIZE>
+__device__ __forceinline__ double sum_squares(const GradTableOf<SIZE>& t, int tid, int block, int blocks) {
   double s = 0.0;
-  for (int c = blockIdx.x; c < t.chunks; c += gridDim.x) {
+  for (int c = block; c < t.chunks; c += blocks) {
     const int i = grad_entry(t, c);
     const int64_t at = (int64_t)(c - t.first[i]) << t.chunk_log2;
     const int n = (int)min((int64_t)1 << t.chunk_log2, t.n[i] - at);
@@ -67,25 +68,32 @@ __global__ void __launch_bounds__(kGradThreads) grad_sumsq_kernel(const GradTabl
       const float* p = static_cast<const float*>(t.src[i]) + at;
       const int h = head_of(p, n), nv = (n - h) / 4, tail = h + nv * 4;
       const f32x4* v = reinterpret_cast<const f32x4*>(p + h);
-      for (int j = threadIdx.x; j < nv; j += kGradThreads) {
+      for (int j = tid; j < nv; j += NT) {
         const f32x4 q = v[j];
         s += (double)q[0] * q[0] + (double)q[1] * q[1] + (double)q[2] * q[2] + (double)q[3] * q[3];
       }
-      if ((int)threadIdx.x < h) s += (double)p[threadIdx.x] * p[threadIdx.x];
-      if (tail + (int)threadIdx.x < n) s += (double)p[tail + threadIdx.x] * p[tail + threadIdx.x];
+      if (tid < h) s += (double)p[tid] * p[tid];
+      if (tail + tid < n) s += (double)p[tail + tid] * p[tail + tid];
     } else {
       const uint16_t* p = static_cast<const uint16_t*>(t.src[i]) + at;
       const int h = head_of(p, n), nv = (n - h) / 8, tail = h + nv * 8;
       const u32x4* v = reinterpret_cast<const u32x4*>(p + h);
-      for (int j = threadIdx.x; j < nv; j += kGradThreads) {
+      for (int j = tid; j < nv; j += NT) {
         const u32x4 q = v[j];
         s += sq2(q[0]) + sq2(q[1]) + sq2(q[2]) + sq2(q[3]);
       }
-      if ((int)threadIdx.x < h) s += sq2(p[threadIdx.x]);
-      if (tail + (int)threadIdx.x < n) s += sq2(p[tail + threadIdx.x]);
+      if (tid < h) s += sq2(p[tid]);
+      if (tail + tid < n) s += sq2(p[tail + tid]);
     }
   }
-  s = block_sum_f64(s, part);
+  return s;
+}
+
+template <int SIZE>
+__global__ void __launch_bounds__(kGradThreads) grad_sumsq_kernel(const GradTableOf<SIZE> t,
+                                                                  double* __restrict__ partial) {
+  __shared__ double part[kGradThreads / kWave];
+  const double s = block_sum_f64(sum_squares<kGradThreads>(t, threadIdx.x, blockIdx.x, gridDim.x), part);
   if (threadIdx.x == 0) partial[blockIdx.x] = s;
 }
 
@@ -104,19 +112,15 @@ __global__ void __launch_bounds__(1024) grad_norm_kernel(const double* __restric
   if (threadIdx.x == 0) *norm = (float)__builtin_sqrt(s);
 }
 
-// Every workgroup sums the partials itself (16 KB, from the L2): no launch
-// between the two passes. The chunks are walked from the last to the first, as
-// the end of what the first pass read is what the caches still hold.
-template <int SIZE>
-__global__ void __launch_bounds__(kGradThreads) grad_scale_kernel(const GradTableOf<SIZE> t,
-                                                                  const double* __restrict__ partial, int np,
-                                                                  double max_norm, float* __restrict__ norm_out) {
-  __shared__ double part[kGradThreads / kWave];
-  const double norm = __builtin_sqrt(sum_partials<kGradThreads>(partial, np, part));
-  if (norm_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
+// out = g * (max_norm / norm) where norm passes max_norm, else g. The chunks are
+// walked from the last to the first, as the end of what the first pass read is
+// what the caches still hold.
+template <int NT, int SIZE>
+__device__ __forceinline__ void scale_gradients(const GradTableOf<SIZE>& t, double norm, double max_norm, int tid,
+                                                int block, int blocks) {
   // a norm that is not finite leaves the gradients as they are
   const double f = norm > max_norm && norm < __builtin_inf() ? max_norm / norm : 1.0;
-  for (int c = t.chunks - 1 - (int)blockIdx.x; c >= 0; c -= gridDim.x) {
+  for (int c = t.chunks - 1 - block; c >= 0; c -= blocks) {
     const int i = grad_entry(t, c);
     if (f == 1.0 && t.src[i] == t.dst[i]) continue;      // in place and nothing to scale
     const int64_t at = (int64_t)(c - t.first[i]) << t.chunk_log2;
@@ -126,30 +130,53 @@ __global__ void __launch_bounds__(kGradThreads) grad_scale_kernel(const GradTabl
       float* o = static_cast<float*>(t.dst[i]) + at;
       const bool same = ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(o)) & 15) == 0;
       const int h = same ? head_of(p, n) : n, nv = (n - h) / 4, tail = h + nv * 4;
-      for (int j = threadIdx.x; j < nv; j += kGradThreads) {
+      for (int j = tid; j < nv; j += NT) {
         f32x4 q = reinterpret_cast<const f32x4*>(p + h)[j];
 #pragma unroll
         for (int k = 0; k < 4; ++k) q[k] = (float)((double)q[k] * f);
         reinterpret_cast<f32x4*>(o + h)[j] = q;
       }
-      for (int j = threadIdx.x; j < h; j += kGradThreads) o[j] = (float)((double)p[j] * f);
-      for (int j = tail + threadIdx.x; j < n; j += kGradThreads) o[j] = (float)((double)p[j] * f);
+      for (int j = tid; j < h; j += NT) o[j] = (float)((double)p[j] * f);
+      for (int j = tail + tid; j < n; j += NT) o[j] = (float)((double)p[j] * f);
     } else {
       const uint16_t* p = static_cast<const uint16_t*>(t.src[i]) + at;
       uint16_t* o = static_cast<uint16_t*>(t.dst[i]) + at;
       const bool same = ((reinterpret_cast<uintptr_t>(p) ^ reinterpret_cast<uintptr_t>(o)) & 15) == 0;
       const int h = same ? head_of(p, n) : n, nv = (n - h) / 8, tail = h + nv * 8;
       auto one = [&](uint32_t b) { return (float)((double)bf16_bits_to_f32(b) * f); };
-      for (int j = threadIdx.x; j < nv; j += kGradThreads) {
+      for (int j = tid; j < nv; j += NT) {
         u32x4 q = reinterpret_cast<const u32x4*>(p + h)[j];
 #pragma unroll
         for (int k = 0; k < 4; ++k) q[k] = cvt_pk_bf16(one(q[k] & 0xFFFFu), one(q[k] >> 16));
         reinterpret_cast<u32x4*>(o + h)[j] = q;
       }
-      for (int j = threadIdx.x; j < h; j += kGradThreads) o[j] = (uint16_t)cvt_pk_bf16(one(p[j]), 0.f);
-      for (int j = tail + threadIdx.x; j < n; j += kGradThreads) o[j] = (uint16_t)cvt_pk_bf16(one(p[j]), 0.f);
+      for (int j = tid; j < h; j += NT) o[j] = (uint16_t)cvt_pk_bf16(one(p[j]), 0.f);
+      for (int j = tail + tid; j < n; j += NT) o[j] = (uint16_t)cvt_pk_bf16(one(p[j]), 0.f);
     }
   }
+}
+
+// Every workgroup sums the partials itself (16 KB, from the L2): no launch
+// between the two passes.
+template <int SIZE>
+__global__ void __launch_bounds__(kGradThreads) grad_scale_kernel(const GradTableOf<SIZE> t,
+                                                                  const double* __restrict__ partial, int np,
+                                                                  double max_norm, float* __restrict__ norm_out) {
+  __shared__ double part[kGradThreads / kWave];
+  const double norm = __builtin_sqrt(sum_partials<kGradThreads>(partial, np, part));
+  if (norm_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *norm_out = (float)norm;
+  scale_gradients<kGradThreads>(t, norm, max_norm, threadIdx.x, blockIdx.x, gridDim.x);
+}
+
+// Few elements (kGradOneMax, ops_api.hip): one workgroup does both passes, a chunk a wave.
+template <int SIZE>
+__global__ void __launch_bounds__(1024) grad_one_kernel(const GradTableOf<SIZE> t, double max_norm, int clip,
+                                                        float* __restrict__ norm_out) {
+  __shared__ double part[16];
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const double norm = __builtin_sqrt(block_sum_f64(sum_squares<kWave>(t, lane, wave, 16), part));
+  if (threadIdx.x == 0) *norm_out = (float)norm;
+  if (clip) scale_gradients<kWave>(t, norm, max_norm, lane, wave, 16);
 }
 
 static GradTableOf<kGradShortTable> short_table(const GradTable& t) {
@@ -173,6 +200,14 @@ hipError_t launch_grad_sumsq(const GradTable& t, int blocks, double* partial, hi
                        partial);
   else
     hipLaunchKernelGGL(grad_sumsq_kernel<kGradTableSize>, dim3(blocks), dim3(kGradThreads), 0, st, t, partial);
+  return hipGetLastError();
+}
+hipError_t launch_grad_one(const GradTable& t, double max_norm, bool clip, float* norm, hipStream_t st) {
+  if (t.count <= kGradShortTable)
+    hipLaunchKernelGGL(grad_one_kernel<kGradShortTable>, dim3(1), dim3(1024), 0, st, short_table(t), max_norm, clip,
+                       norm);
+  else
+    hipLaunchKernelGGL(grad_one_kernel<kGradTableSize>, dim3(1), dim3(1024), 0, st, t, max_norm, clip, norm);
   return hipGetLastError();
 }
 hipError_t launch_grad_norm(const double* partial, int n, float* norm, hipStream_t st) {

@@ -116,6 +116,8 @@ struct GradTableOf {
 typedef GradTableOf<kGradTableSize> GradTable;
 static_assert(sizeof(GradTable) <= 4000, "kernel arguments");
 hipError_t launch_grad_sumsq(const GradTable& t, int blocks, double* partial, hipStream_t st);
+// the norm and (clip) the scaled gradients of one table by one workgroup
+hipError_t launch_grad_one(const GradTable& t, double max_norm, bool clip, float* norm, hipStream_t st);
 hipError_t launch_grad_norm(const double* partial, int n, float* norm, hipStream_t st);
 // norm: where to write the norm (one launch of a call does), or null
 hipError_t launch_grad_scale(const GradTable& t, int blocks, const double* partial, int n, double max_norm, float* norm,

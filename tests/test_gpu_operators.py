@@ -474,7 +474,7 @@ def norm64(ts):
     return float(torch.sqrt(sum((t.double() ** 2).sum() for t in ts)))
 
 
-SIZES = [[1], [7, 0, 33000, 5], [1 << 15, (1 << 15) + 1, 100003], [3] * 301, [2_000_003]]
+SIZES = [[1], [7, 0, 33000, 5], [65536], [65537], [2048] * 32, [2048] * 33, [1, 2, 3] * 40, [500] * 121, [0, 30000, 0, 40001], [1 << 15, (1 << 15) + 1, 100003], [3] * 301, [2_000_003]]
 
 
 @pytest.mark.parametrize("sizes", SIZES)
