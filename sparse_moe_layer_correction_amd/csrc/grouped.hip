@@ -95,12 +95,12 @@ static void launch_form(const GroupedArgs& a, const GroupedPlan& plan, int64_t g
 // expert's last M tile is taken as half used). us of a call, 256 x 256 tiles /
 // 128 x 128 tiles / the latter with four stages:
 //   rows product, R 20000, E 2, [640, 640] (237 big tiles)   22 / 26 / 37
-//   rows product, R 32768, E 128, [2048, 5120]              806 / 999 / 1101
-//   wgrad, R 8000, E 30, [504, 3000] (720 big tiles)         59 / 81 / 104
+//   rows product, R 32768, E 128, [2048, 5120]              819 / 1034 / 1101
+//   wgrad, R 8000, E 30, [504, 3000] (720 big tiles)         68 / 70 / 104 (with dx 119 / 155)
 //   wgrad, R 20000, E 2, [640, 640] (18 big, 50 small)        - / 100 / 62
 //   dgrad, R 2000, E 16, [1200, 400] (124 small tiles)        - / 15.8 / 13.2
-//   rows product, R 17097, E 12, [368, 4952] (144 big tiles)  91 / 98 / 104
-//   wgrad, R 76894, E 329, [112, 560] (half of a big tile)    44 / 33 / -
+//   rows product, R 17097, E 12, [368, 4952] (144 big tiles)  90 / 94 / 104
+//   wgrad, R 76894, E 329, [112, 560] (half of a big tile)    50 / 37 / -
 // So the big tile where its tiles are more than half the 256 CUs' number and
 // compute little beyond the output's edge (kBigPadding times the small tiles'),
 // else the small one, with four stages while every workgroup has a CU to itself
